@@ -14,8 +14,9 @@
  *
  * Conventions shared by every entry point:
  *   - Every pointer is a DEVICE pointer the caller allocated and owns.  The
- *     library allocates no device memory, uses no scratch buffer and never
- *     frees or retains a caller buffer.  Its only state across calls is a
+ *     library allocates no device memory, uses no scratch buffer but the
+ *     workspace that a caller hands to tern_moe, and never frees or retains a
+ *     caller buffer.  Its only state across calls is a
  *     per-process record, per device and kernel instantiation, that the
  *     kernel's dynamic-LDS limit has been raised (hipFuncSetAttribute, done
  *     once on first use); no call's result depends on an earlier call.
@@ -80,6 +81,7 @@ typedef enum {
 
 #define TERN_GROUP 128
 #define TERN_GEMV_MAX_M 4
+#define TERN_MX_BLOCK 32
 /* Size limits: M, N <= 2^31 - 1 and K <= 2^30; M*N, M*K and N*K <= 2^62. */
 
 /* Human-readable name of a status code (a static string; never NULL). */
@@ -208,6 +210,86 @@ tern_status tern_quantize_scales(const uint16_t *scales, int8_t *scales_q, float
 tern_status tern_matmul_s8(const void *X, tern_dtype x_dtype, const uint8_t *packed_W, const int8_t *scales_q,
                            const float *row_factor, void *Y, tern_dtype y_dtype, int64_t M, int64_t N,
                            int64_t K, int32_t group, tern_path path, hipStream_t stream);
+
+/*
+ * Microscaled 4-bit floats (the OCP MX format with e2m1 elements), for the
+ * layers that a mixed-precision ternary model keeps at more than two bits.
+ * A matrix [R,K], K % 32 == 0 (TERN_ERR_GROUP otherwise), is held as
+ *   codes [R,K/2] uint8: two 4-bit codes a byte, the even element in the low
+ *       nibble; a code is a sign bit and one of the magnitudes 0, 0.5, 1,
+ *       1.5, 2, 3, 4, 6;
+ *   exps [R,K/32] uint8: one per 32 consecutive elements of a row; the scale
+ *       is 2^(exps - 127), and 255 makes the block NaN.
+ * codes and the dense matrix: 16-byte aligned; exps: any alignment.
+ */
+
+/*
+ * tern_mx_quantize -- X[M,K] (TERN_F16, TERN_BF16 or TERN_F32) -> codes, exps.
+ * A block with the largest magnitude a gets the scale 2^E, E = max(floor(
+ * log2 a) - 2, -127); each element is rounded to the nearest magnitude of
+ * element / 2^E, ties to the even code, and to 6 if it lies above.  A zero
+ * block gets the byte 0.  A block with an infinity or a NaN gets the byte 255
+ * and zero codes, and reads back as NaN.
+ */
+tern_status tern_mx_quantize(const void *X, tern_dtype x_dtype, uint8_t *codes, uint8_t *exps, int64_t M, int64_t K,
+                             hipStream_t stream);
+
+/*
+ * tern_mx_dequant -- codes, exps -> W[M,K] in w_dtype.  Exact in TERN_F32 and
+ * TERN_BF16; in TERN_F16 rounded to nearest even where the value leaves the
+ * type's range.
+ */
+tern_status tern_mx_dequant(const uint8_t *codes, const uint8_t *exps, void *W, tern_dtype w_dtype, int64_t M,
+                            int64_t K, hipStream_t stream);
+
+/*
+ * tern_mx_matmul -- Y[M,N] = X[M,K] . W^T, W[N,K] held as codes and exps,
+ * X in TERN_F16 or TERN_BF16, sums in fp32, Y in any of the three types,
+ * rounded once (nearest even).  Any M.  X 16-byte aligned, Y to its element.
+ * The products are exact.  An infinity or NaN in a row of X reaches that row
+ * of Y only, one in a row of W (a block with exponent 255, or values beyond
+ * the fp32 range) that column only.
+ */
+tern_status tern_mx_matmul(const void *X, tern_dtype x_dtype, const uint8_t *codes, const uint8_t *exps, void *Y,
+                           tern_dtype y_dtype, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * tern_mx_matmul_mx -- the same product with X[M,K] held as x_codes and
+ * x_exps too (for instance from tern_mx_quantize).
+ */
+tern_status tern_mx_matmul_mx(const uint8_t *x_codes, const uint8_t *x_exps, const uint8_t *codes,
+                              const uint8_t *exps, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,
+                              hipStream_t stream);
+
+/*
+ * tern_moe -- a mixture-of-experts layer with ternary experts, for the few
+ * tokens of a decode step:
+ *   y[t] = sum over e in S(t) of w[t,e] * Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t]))
+ * S(t): the top_k experts by logit (ties to the lowest index; an expert whose
+ * logit is -inf is never taken, so a token whose logits are all -inf, such as
+ * padding, gets y = 0).  w: softmax of the logits, over S(t) if renormalize
+ * is not 0, else over all experts.  A NaN counts as the largest logit; a row
+ * with a NaN or +inf has NaN weights.
+ *   X [T,H] TERN_F16 or TERN_BF16, logits [T,E] and Y [T,H] of any type
+ *   gate_up [E,2F,H/4] tern_pack codes, rows 0..F-1 of an expert Wg and
+ *       F..2F-1 Wu; gate_up_scales [E,2F,H/128] fp16
+ *   down [E,H,F/4], down_scales [E,H,F/128]: Wd
+ *   group must be 128 and divide H and F; 1 <= top_k <= min(E, 32) and
+ *   E <= 1024 (TERN_ERR_UNSUPPORTED beyond those two limits).
+ *   workspace: tern_moe_workspace bytes (TERN_ERR_SHAPE if fewer), 256-byte
+ *       aligned, for this call alone until the stream has passed it.
+ * Hidden values and all sums are fp32; Y is rounded once.  Any T; tokens are
+ * taken 64 at a time, each time reading the experts that they take.  The
+ * result of a token does not depend on the other tokens of its call beyond
+ * the order in which fp32 sums are formed, and repeated calls agree bit for
+ * bit.
+ */
+size_t tern_moe_workspace(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F);
+tern_status tern_moe(const void *X, tern_dtype x_dtype, const void *logits, tern_dtype l_dtype,
+                     const uint8_t *gate_up, const uint16_t *gate_up_scales, const uint8_t *down,
+                     const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E, int64_t top_k,
+                     int64_t H, int64_t F, int32_t group, int32_t renormalize, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream);
 
 /*
  * tern_stream_copy -- calibration, not part of the method: stream `bytes`

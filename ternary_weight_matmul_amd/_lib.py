@@ -70,6 +70,19 @@ def _load() -> ctypes.CDLL:
     L.tern_quantize_scales.restype = c_int
     L.tern_matmul_s8.argtypes = [vp, c_int, vp, vp, vp, vp, c_int, i64, i64, i64, i32, c_int, vp]
     L.tern_matmul_s8.restype = c_int
+    L.tern_mx_quantize.argtypes = [vp, c_int, vp, vp, i64, i64, vp]
+    L.tern_mx_quantize.restype = c_int
+    L.tern_mx_dequant.argtypes = [vp, vp, vp, c_int, i64, i64, vp]
+    L.tern_mx_dequant.restype = c_int
+    L.tern_mx_matmul.argtypes = [vp, c_int, vp, vp, vp, c_int, i64, i64, i64, vp]
+    L.tern_mx_matmul.restype = c_int
+    L.tern_mx_matmul_mx.argtypes = [vp, vp, vp, vp, vp, c_int, i64, i64, i64, vp]
+    L.tern_mx_matmul_mx.restype = c_int
+    L.tern_moe_workspace.argtypes = [i64, i64, i64, i64, i64]
+    L.tern_moe_workspace.restype = ctypes.c_size_t
+    L.tern_moe.argtypes = [vp, c_int, vp, c_int, vp, vp, vp, vp, vp, c_int, i64, i64, i64, i64, i64, i32, i32, vp,
+                           ctypes.c_size_t, vp]
+    L.tern_moe.restype = c_int
     L.tern_stream_copy.argtypes = [vp, vp, ctypes.c_uint64, vp]
     L.tern_stream_copy.restype = c_int
     return L

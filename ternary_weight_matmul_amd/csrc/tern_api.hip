@@ -5,6 +5,8 @@
 
 #include "../../include/tern.h"
 #include "tern_kernels.h"
+#include "tern_moe.h"
+#include "tern_mx.h"
 
 namespace {
 
@@ -145,6 +147,66 @@ hipError_t dispatch(const tern::GemmArgs &a, tern_path path) {
     }
 }
 
+int dtype_index(tern_dtype d) { return d == TERN_F16 ? 0 : (d == TERN_BF16 ? 1 : 2); }
+
+bool known_dtype(tern_dtype d) { return d == TERN_F16 || d == TERN_BF16 || d == TERN_F32; }
+
+// A microscaled matrix [rows, K] and, beside it, the dense one it comes from or goes to.
+tern_status check_mx_args(const void *codes, const void *exps, const void *dense, tern_dtype dtype, int64_t rows,
+                          int64_t K) {
+    if (rows < 0 || K < 0 || rows > kMaxDim || K > kMaxK || !product_ok(rows, K)) return TERN_ERR_SHAPE;
+    if (K % TERN_MX_BLOCK != 0) return TERN_ERR_GROUP;
+    if (!known_dtype(dtype)) return TERN_ERR_DTYPE;
+    if (rows == 0 || K == 0) return TERN_OK;
+    if (codes == nullptr || exps == nullptr || dense == nullptr) return TERN_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(dense, 16)) return TERN_ERR_ALIGN;
+    return TERN_OK;
+}
+
+// Both products: XE is null where X holds 16-bit values.
+tern_status check_mx_product(const void *X, const void *XE, bool mx, const void *W, const void *WE, const void *Y,
+                             tern_dtype y_dtype, int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return TERN_ERR_SHAPE;
+    if (!product_ok(M, N) || !product_ok(M, K) || !product_ok(N, K)) return TERN_ERR_SHAPE;
+    if (K % TERN_MX_BLOCK != 0) return TERN_ERR_GROUP;
+    if (!known_dtype(y_dtype)) return TERN_ERR_DTYPE;
+    if (M == 0 || N == 0) return TERN_OK;
+    if (Y == nullptr) return TERN_ERR_NULL;
+    if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
+    if (K == 0) return TERN_OK;
+    if (X == nullptr || W == nullptr || WE == nullptr || (mx && XE == nullptr)) return TERN_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(W, 16)) return TERN_ERR_ALIGN;
+    return TERN_OK;
+}
+
+tern_status mx_product(const void *X, const uint8_t *XE, int x_dtype, const uint8_t *W, const uint8_t *WE, void *Y,
+                       tern_dtype y_dtype, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+    const tern_status st = check_mx_product(X, XE, x_dtype == 2, W, WE, Y, y_dtype, M, N, K);
+    if (st != TERN_OK || M == 0 || N == 0) return st;
+    if (K == 0) return from_hip(tern::launch_fill_zero(Y, M * N * (int64_t)dtype_size(y_dtype), stream));
+    tern::MxArgs a;
+    a.X = X;
+    a.XE = XE;
+    a.x_dtype = x_dtype;
+    a.W = W;
+    a.WE = WE;
+    a.Y = Y;
+    a.y_dtype = dtype_index(y_dtype);
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.stream = stream;
+    return from_hip(tern::launch_mx_gemv(a));
+}
+
+bool moe_sizes_ok(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {
+    if (T < 0 || E < 0 || top_k < 0 || H < 0 || F < 0) return false;
+    if (T > kMaxDim || E > kMaxDim || top_k > kMaxDim || H > kMaxK || F > kMaxK) return false;
+    // 2 E F H weights, T H and T E values, pairs * (F + H) floats of workspace
+    return product_ok(H, F) && product_ok(2 * E, H * F) && product_ok(T, H) && product_ok(T, E) &&
+           product_ok(top_k, (H + F) * tern::kMoeChunk * 8);
+}
+
 }  // namespace
 
 extern "C" {
@@ -265,6 +327,80 @@ tern_status tern_dequant(const uint8_t *packed, const uint16_t *scales, void *W,
     if (packed == nullptr || scales == nullptr || W == nullptr) return TERN_ERR_NULL;
     if (!aligned(packed, 16) || !aligned(W, 16) || !aligned(scales, 2)) return TERN_ERR_ALIGN;
     return from_hip(tern::launch_dequant(packed, scales, W, w_dtype == TERN_BF16 ? 1 : 0, N, K, stream));
+}
+
+tern_status tern_mx_quantize(const void *X, tern_dtype x_dtype, uint8_t *codes, uint8_t *exps, int64_t M, int64_t K,
+                             hipStream_t stream) {
+    const tern_status st = check_mx_args(codes, exps, X, x_dtype, M, K);
+    if (st != TERN_OK || M == 0 || K == 0) return st;
+    return from_hip(tern::launch_mx_quantize(X, dtype_index(x_dtype), codes, exps, M * (K / TERN_MX_BLOCK), stream));
+}
+
+tern_status tern_mx_dequant(const uint8_t *codes, const uint8_t *exps, void *W, tern_dtype w_dtype, int64_t M,
+                            int64_t K, hipStream_t stream) {
+    const tern_status st = check_mx_args(codes, exps, W, w_dtype, M, K);
+    if (st != TERN_OK || M == 0 || K == 0) return st;
+    return from_hip(tern::launch_mx_dequant(codes, exps, W, dtype_index(w_dtype), M * (K / TERN_MX_BLOCK), stream));
+}
+
+tern_status tern_mx_matmul(const void *X, tern_dtype x_dtype, const uint8_t *codes, const uint8_t *exps, void *Y,
+                           tern_dtype y_dtype, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+    if (x_dtype != TERN_F16 && x_dtype != TERN_BF16) return TERN_ERR_DTYPE;
+    return mx_product(X, nullptr, dtype_index(x_dtype), codes, exps, Y, y_dtype, M, N, K, stream);
+}
+
+tern_status tern_mx_matmul_mx(const uint8_t *x_codes, const uint8_t *x_exps, const uint8_t *codes,
+                              const uint8_t *exps, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,
+                              hipStream_t stream) {
+    return mx_product(x_codes, x_exps, 2, codes, exps, Y, y_dtype, M, N, K, stream);
+}
+
+size_t tern_moe_workspace(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {
+    if (!moe_sizes_ok(T, E, top_k, H, F) || T == 0 || H == 0 || F == 0 || top_k > tern::kMoeMaxTopK) return 0;
+    return tern::moe_workspace(T, top_k, H, F);
+}
+
+tern_status tern_moe(const void *X, tern_dtype x_dtype, const void *logits, tern_dtype l_dtype,
+                     const uint8_t *gate_up, const uint16_t *gate_up_scales, const uint8_t *down,
+                     const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E, int64_t top_k,
+                     int64_t H, int64_t F, int32_t group, int32_t renormalize, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+    if (!moe_sizes_ok(T, E, top_k, H, F) || top_k < 1 || top_k > E) return TERN_ERR_SHAPE;
+    if (group <= 0 || H % group != 0 || F % group != 0) return TERN_ERR_GROUP;
+    if (x_dtype != TERN_F16 && x_dtype != TERN_BF16) return TERN_ERR_DTYPE;
+    if (!known_dtype(l_dtype) || !known_dtype(y_dtype)) return TERN_ERR_DTYPE;
+    if (group != TERN_GROUP || E > tern::kMoeMaxExperts || top_k > tern::kMoeMaxTopK) return TERN_ERR_UNSUPPORTED;
+    if (T == 0 || H == 0) return TERN_OK;
+    if (Y == nullptr) return TERN_ERR_NULL;
+    if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
+    if (F == 0) return from_hip(tern::launch_fill_zero(Y, T * H * (int64_t)dtype_size(y_dtype), stream));
+    if (X == nullptr || logits == nullptr || gate_up == nullptr || gate_up_scales == nullptr || down == nullptr ||
+        down_scales == nullptr || workspace == nullptr)
+        return TERN_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(logits, dtype_size(l_dtype)) || !aligned(gate_up, 16) || !aligned(down, 16) ||
+        !aligned(gate_up_scales, 2) || !aligned(down_scales, 2) || !aligned(workspace, 256))
+        return TERN_ERR_ALIGN;
+    if (workspace_bytes < tern::moe_workspace(T, top_k, H, F)) return TERN_ERR_SHAPE;
+    tern::MoeArgs a;
+    a.X = X;
+    a.x_dtype = dtype_index(x_dtype);
+    a.logits = logits;
+    a.l_dtype = dtype_index(l_dtype);
+    a.GU = gate_up;
+    a.GUS = gate_up_scales;
+    a.D = down;
+    a.DS = down_scales;
+    a.Y = Y;
+    a.y_dtype = dtype_index(y_dtype);
+    a.T = T;
+    a.E = E;
+    a.top_k = top_k;
+    a.H = H;
+    a.F = F;
+    a.renormalize = renormalize;
+    a.ws = workspace;
+    a.stream = stream;
+    return from_hip(tern::launch_moe(a));
 }
 
 }  // extern "C"

@@ -207,6 +207,153 @@ def matmul_s8(x: torch.Tensor, packed: torch.Tensor, scales_q: torch.Tensor, row
     return matmul_s8_into(x, packed, scales_q, row_factor, out, group, path)
 
 
+# --- microscaled 4-bit floats ---------------------------------------------------
+
+def _same_device(t: torch.Tensor, **others: torch.Tensor) -> None:
+    for name, o in others.items():
+        if o.device != t.device:
+            raise ValueError(f"{name} is on {o.device}, expected {t.device}")
+
+
+def _need_float(t: torch.Tensor, name: str, dtypes) -> None:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    _need(t, name, t.dtype)
+
+
+def _mx_shape(codes: torch.Tensor, exps: torch.Tensor, names: str):
+    """(rows, K) of a matrix held as codes and exps."""
+    _need(codes, names.split()[0], torch.uint8)
+    _need(exps, names.split()[1], torch.uint8)
+    rows, half = codes.shape
+    if tuple(exps.shape) != (rows, half // 16) or half % 16 != 0:
+        raise ValueError(f"shape mismatch: {names} {tuple(codes.shape)}, {tuple(exps.shape)}; "
+                         "expected [R, K/2] and [R, K/32]")
+    return rows, 2 * half
+
+
+def mx_quantize(x: torch.Tensor):
+    """x [M,K] fp16/bf16/fp32 -> (codes uint8 [M,K/2], exps uint8 [M,K/32]): e2m1 values with a
+    power-of-two scale per 32, rounded to nearest even (tern_mx_quantize)."""
+    _need_float(x, "x", tuple(_TORCH_CODE))
+    M, K = x.shape
+    with torch.cuda.device(x.device):
+        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        exps = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+        _check(lib.tern_mx_quantize(x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(), exps.data_ptr(), M, K,
+                                    _stream(x)), "tern_mx_quantize")
+    return codes, exps
+
+
+def mx_dequant(codes: torch.Tensor, exps: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values [M,K] of a matrix held as codes and exps; exact in fp32 and bf16."""
+    M, K = _mx_shape(codes, exps, "codes exps")
+    if out is None:
+        if out_dtype not in _TORCH_CODE:
+            raise TypeError("out_dtype must be float32, bfloat16 or float16")
+        out = torch.empty((M, K), dtype=out_dtype, device=codes.device)
+    _need_float(out, "out", tuple(_TORCH_CODE))
+    if tuple(out.shape) != (M, K):
+        raise ValueError("out must be [M, K]")
+    _same_device(codes, exps=exps, out=out)
+    with torch.cuda.device(codes.device):
+        _check(lib.tern_mx_dequant(codes.data_ptr(), exps.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, K,
+                                   _stream(codes)), "tern_mx_dequant")
+    return out
+
+
+def mx_matmul_into(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
+    """out[M,N] = x[M,K] . W^T, x fp16/bf16, W [N,K] held as codes and exps."""
+    _need_float(x, "x", (torch.float16, torch.bfloat16))
+    _need_float(out, "out", tuple(_TORCH_CODE))
+    N, K = _mx_shape(codes, exps, "codes exps")
+    M = x.shape[0]
+    if x.shape[1] != K or tuple(out.shape) != (M, N):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, codes {tuple(codes.shape)}, out {tuple(out.shape)}")
+    _same_device(x, codes=codes, exps=exps, out=out)
+    with torch.cuda.device(x.device):
+        _check(lib.tern_mx_matmul(x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(), exps.data_ptr(),
+                                  out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, _stream(x)), "tern_mx_matmul")
+    return out
+
+
+def mx_matmul(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
+              out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Y[M,N] = x[M,K] . W^T with fp32 accumulation, W [N,K] held as codes and exps; returns a new tensor."""
+    out = torch.empty((x.shape[0], codes.shape[0]), dtype=out_dtype, device=x.device)
+    return mx_matmul_into(x, codes, exps, out)
+
+
+def mx_matmul_mx_into(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
+                      out: torch.Tensor) -> torch.Tensor:
+    """out[M,N] = X . W^T with both matrices held as codes and exps."""
+    _need_float(out, "out", tuple(_TORCH_CODE))
+    M, K = _mx_shape(x_codes, x_exps, "x_codes x_exps")
+    N, KW = _mx_shape(codes, exps, "codes exps")
+    if K != KW or tuple(out.shape) != (M, N):
+        raise ValueError(f"shape mismatch: x_codes {tuple(x_codes.shape)}, codes {tuple(codes.shape)}, "
+                         f"out {tuple(out.shape)}")
+    _same_device(x_codes, x_exps=x_exps, codes=codes, exps=exps, out=out)
+    with torch.cuda.device(x_codes.device):
+        _check(lib.tern_mx_matmul_mx(x_codes.data_ptr(), x_exps.data_ptr(), codes.data_ptr(), exps.data_ptr(),
+                                     out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, _stream(x_codes)),
+               "tern_mx_matmul_mx")
+    return out
+
+
+def mx_matmul_mx(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
+                 out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Y[M,N] = X . W^T with both matrices held as codes and exps; returns a new tensor."""
+    out = torch.empty((x_codes.shape[0], codes.shape[0]), dtype=out_dtype, device=x_codes.device)
+    return mx_matmul_mx_into(x_codes, x_exps, codes, exps, out)
+
+
+# --- mixture of ternary experts -------------------------------------------------
+
+def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
+             down: torch.Tensor, down_scales: torch.Tensor, out: torch.Tensor, top_k: int,
+             renormalize: bool = True, group: int = 128) -> torch.Tensor:
+    """out [T,H] = the mixture-of-experts layer of tern_moe: x [T,H] fp16/bf16, logits [T,E],
+    gate_up [E,2F,H/4] and down [E,H,F/4] packed codes, their fp16 scales one per 128."""
+    _need_float(x, "x", (torch.float16, torch.bfloat16))
+    _need_float(logits, "logits", tuple(_TORCH_CODE))
+    _need_float(out, "out", tuple(_TORCH_CODE))
+    _need(gate_up, "gate_up", torch.uint8, ndim=3)
+    _need(gate_up_scales, "gate_up_scales", torch.float16, ndim=3)
+    _need(down, "down", torch.uint8, ndim=3)
+    _need(down_scales, "down_scales", torch.float16, ndim=3)
+    T, H = x.shape
+    E, F = gate_up.shape[0], down.shape[2] * 4
+    if group <= 0:
+        raise ValueError("group must be positive")
+    want = {"logits": (logits, (T, E)), "gate_up": (gate_up, (E, 2 * F, H // 4)),
+            "gate_up_scales": (gate_up_scales, (E, 2 * F, H // group)), "down": (down, (E, H, F // 4)),
+            "down_scales": (down_scales, (E, H, F // group)), "out": (out, (T, H))}
+    for name, (t, shape) in want.items():
+        if tuple(t.shape) != shape:
+            raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {shape}")
+        _same_device(x, **{name: t})
+    with torch.cuda.device(x.device):
+        nbytes = lib.tern_moe_workspace(T, E, top_k, H, F)
+        # on the current stream: torch's allocator keeps it for this call until the stream has passed it,
+        # and inside a graph capture it belongs to the graph
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
+        _check(lib.tern_moe(x.data_ptr(), _TORCH_CODE[x.dtype], logits.data_ptr(), _TORCH_CODE[logits.dtype],
+                            gate_up.data_ptr(), gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(),
+                            out.data_ptr(), _TORCH_CODE[out.dtype], T, E, top_k, H, F, group, int(renormalize),
+                            ws.data_ptr(), nbytes, _stream(x)), "tern_moe")
+    return out
+
+
+def moe(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
+        down: torch.Tensor, down_scales: torch.Tensor, top_k: int, renormalize: bool = True,
+        out_dtype: Optional[torch.dtype] = None, group: int = 128) -> torch.Tensor:
+    """The layer's outputs [T,H] (of x's type unless out_dtype is given) as a new tensor."""
+    out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    return moe_into(x, logits, gate_up, gate_up_scales, down, down_scales, out, top_k, renormalize, group)
+
+
 # --- one GPU's share of a sharded layer (no communication here) -------------
 
 def shard_columns(packed: torch.Tensor, scales: torch.Tensor, rank: int, world: int):
