@@ -1,0 +1,66 @@
+// tern_mx_device.h -- device helpers shared by the products with microscaled
+// 4-bit weights.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "tern_device.h"
+
+namespace tern {
+
+typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const bf162_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// bf16 hi (term 0) or lo (term 1) of 8 fp16 values.  hi + lo is the value
+// exactly: hi keeps 8 of its 11 significant bits and lo the rest.  An
+// infinity would leave inf - inf in lo: its lo is 0.
+__device__ __forceinline__ uint4 fp16_term(const uint4 &q, bool lo) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = f16_bits_to_float((uint16_t)w[i]), b = f16_bits_to_float((uint16_t)(w[i] >> 16));
+        const uint32_t hi = bf16_pair(a, b);
+        const float ah = __builtin_bit_cast(float, hi << 16), bh = __builtin_bit_cast(float, hi & 0xFFFF0000u);
+        const uint32_t rest = bf16_pair(a == ah ? 0.f : a - ah, b == bh ? 0.f : b - bh);
+        o[i] = lo ? rest : hi;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 8 e2m1 codes -> 8 bf16 values times the scale s (exact: two significant bits).
+__device__ __forceinline__ bf168_t decode8(uint32_t c, float s) {
+    uint32_t w[4];
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+    return __builtin_bit_cast(bf168_t, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// Raise a kernel's dynamic-LDS limit once per device and kernel (a per-process
+// attribute; not a stream operation).
+template <auto Kern>
+inline hipError_t raise_lds_limit(size_t lds) {
+    if (lds <= 64 * 1024) return hipSuccess;
+    static std::atomic<uint64_t> done_mask{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done_mask.load(std::memory_order_acquire) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e != hipSuccess) return e;
+        done_mask.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return hipSuccess;
+}
+
+}  // namespace tern

@@ -25,12 +25,12 @@
 
 #include "tern_device.h"
 #include "tern_mx.h"
+#include "tern_mx_device.h"
 
 namespace tern {
 
 namespace {
 
-typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
 typedef float float4v_t __attribute__((ext_vector_type(4)));
 typedef int int8v_t __attribute__((ext_vector_type(8)));
 
@@ -39,38 +39,6 @@ constexpr int G_MAX_WAVES = 16;
 
 // Activation rows of one matrix tile: 8 slots; an fp16 row takes two.
 constexpr int rows_per_set(int xt) { return xt == 0 ? 4 : 8; }
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    const bf162_t v = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-// bf16 hi (term 0) or lo (term 1) of 8 fp16 values.  hi + lo is the value
-// exactly: hi keeps 8 of its 11 significant bits and lo the rest.  An
-// infinity would leave inf - inf in lo: its lo is 0.
-__device__ __forceinline__ uint4 fp16_term(const uint4 &q, bool lo) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = f16_bits_to_float((uint16_t)w[i]), b = f16_bits_to_float((uint16_t)(w[i] >> 16));
-        const uint32_t hi = bf16_pair(a, b);
-        const float ah = __builtin_bit_cast(float, hi << 16), bh = __builtin_bit_cast(float, hi & 0xFFFF0000u);
-        const uint32_t rest = bf16_pair(a == ah ? 0.f : a - ah, b == bh ? 0.f : b - bh);
-        o[i] = lo ? rest : hi;
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-// 8 e2m1 codes -> 8 bf16 values times the scale s.
-__device__ __forceinline__ bf168_t decode8(uint32_t c, float s) {
-    uint32_t w[4];
-    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
-    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
-    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
-    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
-    return __builtin_bit_cast(bf168_t, make_uint4(w[0], w[1], w[2], w[3]));
-}
 
 template <int XT, int SETS, int NB>
 struct Stage {

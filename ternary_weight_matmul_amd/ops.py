@@ -208,73 +208,101 @@ def matmul_s8(x: torch.Tensor, packed: torch.Tensor, scales_q: torch.Tensor, row
 
 
 # --- microscaled 4-bit floats ---------------------------------------------------
+#
+# A decode step calls these once per layer with microseconds of GPU work, so
+# the binding's own time counts: the checks are single expressions, and the
+# stream and the device are read through the raw accessors (0.1 us each where
+# torch.cuda.current_stream and torch.cuda.device take 2.0 and 1.4).
 
-def _same_device(t: torch.Tensor, **others: torch.Tensor) -> None:
-    for name, o in others.items():
-        if o.device != t.device:
-            raise ValueError(f"{name} is on {o.device}, expected {t.device}")
+_FLOAT16S = (torch.float16, torch.bfloat16)
+_FLOATS = tuple(_TORCH_CODE)
 
 
-def _need_float(t: torch.Tensor, name: str, dtypes) -> None:
+def _launch(fn, where: str, t: torch.Tensor, *args) -> None:
+    """fn(*args, stream) on t's device and its current stream."""
+    index = t.get_device()
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        raise TernError(status, where)
+
+
+def _need_at(t: torch.Tensor, name: str, device: torch.device, dtypes, shape) -> None:
+    """t lies on `device`, dense, with one of the types and the shape."""
+    if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on the device of the other tensors, {device}; it is on {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    _need(t, name, t.dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous (call .contiguous())")
 
 
-def _mx_shape(codes: torch.Tensor, exps: torch.Tensor, names: str):
-    """(rows, K) of a matrix held as codes and exps."""
-    _need(codes, names.split()[0], torch.uint8)
-    _need(exps, names.split()[1], torch.uint8)
+def _need_matrix(t: torch.Tensor, name: str, dtypes) -> None:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not (t.is_cuda and t.dim() == 2 and t.is_contiguous()):
+        _need(t, name, t.dtype)
+
+
+_U8 = (torch.uint8,)
+_F16 = (torch.float16,)
+
+
+def _need_codes(codes: torch.Tensor, exps: torch.Tensor, device: torch.device, prefix: str = ""):
+    """(rows, K) of a matrix held as codes and exps on `device`."""
+    _need_matrix(codes, prefix + "codes", _U8)
     rows, half = codes.shape
-    if tuple(exps.shape) != (rows, half // 16) or half % 16 != 0:
-        raise ValueError(f"shape mismatch: {names} {tuple(codes.shape)}, {tuple(exps.shape)}; "
-                         "expected [R, K/2] and [R, K/32]")
+    if half % 16 != 0:
+        raise ValueError(f"{prefix}codes must be [R, K/2] with K a multiple of 32, got {tuple(codes.shape)}")
+    _need_at(codes, prefix + "codes", device, _U8, (rows, half))
+    _need_at(exps, prefix + "exps", device, _U8, (rows, half // 16))
     return rows, 2 * half
 
 
 def mx_quantize(x: torch.Tensor):
     """x [M,K] fp16/bf16/fp32 -> (codes uint8 [M,K/2], exps uint8 [M,K/32]): e2m1 values with a
     power-of-two scale per 32, rounded to nearest even (tern_mx_quantize)."""
-    _need_float(x, "x", tuple(_TORCH_CODE))
+    _need_matrix(x, "x", _FLOATS)
     M, K = x.shape
-    with torch.cuda.device(x.device):
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-        exps = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-        _check(lib.tern_mx_quantize(x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(), exps.data_ptr(), M, K,
-                                    _stream(x)), "tern_mx_quantize")
+    device = x.device
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=device)
+    exps = torch.empty((M, K // 32), dtype=torch.uint8, device=device)
+    _launch(lib.tern_mx_quantize, "tern_mx_quantize", x, x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(),
+            exps.data_ptr(), M, K)
     return codes, exps
 
 
 def mx_dequant(codes: torch.Tensor, exps: torch.Tensor, out_dtype: torch.dtype = torch.float32,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values [M,K] of a matrix held as codes and exps; exact in fp32 and bf16."""
-    M, K = _mx_shape(codes, exps, "codes exps")
+    M, K = _need_codes(codes, exps, codes.device)
     if out is None:
         if out_dtype not in _TORCH_CODE:
             raise TypeError("out_dtype must be float32, bfloat16 or float16")
         out = torch.empty((M, K), dtype=out_dtype, device=codes.device)
-    _need_float(out, "out", tuple(_TORCH_CODE))
-    if tuple(out.shape) != (M, K):
-        raise ValueError("out must be [M, K]")
-    _same_device(codes, exps=exps, out=out)
-    with torch.cuda.device(codes.device):
-        _check(lib.tern_mx_dequant(codes.data_ptr(), exps.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, K,
-                                   _stream(codes)), "tern_mx_dequant")
+    else:
+        _need_at(out, "out", codes.device, _FLOATS, (M, K))
+    _launch(lib.tern_mx_dequant, "tern_mx_dequant", codes, codes.data_ptr(), exps.data_ptr(), out.data_ptr(),
+            _TORCH_CODE[out.dtype], M, K)
     return out
 
 
 def mx_matmul_into(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
     """out[M,N] = x[M,K] . W^T, x fp16/bf16, W [N,K] held as codes and exps."""
-    _need_float(x, "x", (torch.float16, torch.bfloat16))
-    _need_float(out, "out", tuple(_TORCH_CODE))
-    N, K = _mx_shape(codes, exps, "codes exps")
+    _need_matrix(x, "x", _FLOAT16S)
+    N, K = _need_codes(codes, exps, x.device)
     M = x.shape[0]
-    if x.shape[1] != K or tuple(out.shape) != (M, N):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, codes {tuple(codes.shape)}, out {tuple(out.shape)}")
-    _same_device(x, codes=codes, exps=exps, out=out)
-    with torch.cuda.device(x.device):
-        _check(lib.tern_mx_matmul(x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(), exps.data_ptr(),
-                                  out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, _stream(x)), "tern_mx_matmul")
+    if x.shape[1] != K:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, codes {tuple(codes.shape)}")
+    _need_at(out, "out", x.device, _FLOATS, (M, N))
+    _launch(lib.tern_mx_matmul, "tern_mx_matmul", x, x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(),
+            exps.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K)
     return out
 
 
@@ -288,17 +316,13 @@ def mx_matmul(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
 def mx_matmul_mx_into(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
                       out: torch.Tensor) -> torch.Tensor:
     """out[M,N] = X . W^T with both matrices held as codes and exps."""
-    _need_float(out, "out", tuple(_TORCH_CODE))
-    M, K = _mx_shape(x_codes, x_exps, "x_codes x_exps")
-    N, KW = _mx_shape(codes, exps, "codes exps")
-    if K != KW or tuple(out.shape) != (M, N):
-        raise ValueError(f"shape mismatch: x_codes {tuple(x_codes.shape)}, codes {tuple(codes.shape)}, "
-                         f"out {tuple(out.shape)}")
-    _same_device(x_codes, x_exps=x_exps, codes=codes, exps=exps, out=out)
-    with torch.cuda.device(x_codes.device):
-        _check(lib.tern_mx_matmul_mx(x_codes.data_ptr(), x_exps.data_ptr(), codes.data_ptr(), exps.data_ptr(),
-                                     out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, _stream(x_codes)),
-               "tern_mx_matmul_mx")
+    M, K = _need_codes(x_codes, x_exps, x_codes.device, "x_")
+    N, KW = _need_codes(codes, exps, x_codes.device)
+    if K != KW:
+        raise ValueError(f"shape mismatch: x_codes {tuple(x_codes.shape)}, codes {tuple(codes.shape)}")
+    _need_at(out, "out", x_codes.device, _FLOATS, (M, N))
+    _launch(lib.tern_mx_matmul_mx, "tern_mx_matmul_mx", x_codes, x_codes.data_ptr(), x_exps.data_ptr(),
+            codes.data_ptr(), exps.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K)
     return out
 
 
@@ -316,33 +340,28 @@ def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_
              renormalize: bool = True, group: int = 128) -> torch.Tensor:
     """out [T,H] = the mixture-of-experts layer of tern_moe: x [T,H] fp16/bf16, logits [T,E],
     gate_up [E,2F,H/4] and down [E,H,F/4] packed codes, their fp16 scales one per 128."""
-    _need_float(x, "x", (torch.float16, torch.bfloat16))
-    _need_float(logits, "logits", tuple(_TORCH_CODE))
-    _need_float(out, "out", tuple(_TORCH_CODE))
-    _need(gate_up, "gate_up", torch.uint8, ndim=3)
-    _need(gate_up_scales, "gate_up_scales", torch.float16, ndim=3)
-    _need(down, "down", torch.uint8, ndim=3)
-    _need(down_scales, "down_scales", torch.float16, ndim=3)
-    T, H = x.shape
-    E, F = gate_up.shape[0], down.shape[2] * 4
+    _need_matrix(x, "x", _FLOAT16S)
+    if gate_up.dim() != 3 or down.dim() != 3:
+        raise ValueError("gate_up must be [E, 2F, H/4] and down [E, H, F/4]")
     if group <= 0:
         raise ValueError("group must be positive")
-    want = {"logits": (logits, (T, E)), "gate_up": (gate_up, (E, 2 * F, H // 4)),
-            "gate_up_scales": (gate_up_scales, (E, 2 * F, H // group)), "down": (down, (E, H, F // 4)),
-            "down_scales": (down_scales, (E, H, F // group)), "out": (out, (T, H))}
-    for name, (t, shape) in want.items():
-        if tuple(t.shape) != shape:
-            raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {shape}")
-        _same_device(x, **{name: t})
-    with torch.cuda.device(x.device):
-        nbytes = lib.tern_moe_workspace(T, E, top_k, H, F)
-        # on the current stream: torch's allocator keeps it for this call until the stream has passed it,
-        # and inside a graph capture it belongs to the graph
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
-        _check(lib.tern_moe(x.data_ptr(), _TORCH_CODE[x.dtype], logits.data_ptr(), _TORCH_CODE[logits.dtype],
-                            gate_up.data_ptr(), gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(),
-                            out.data_ptr(), _TORCH_CODE[out.dtype], T, E, top_k, H, F, group, int(renormalize),
-                            ws.data_ptr(), nbytes, _stream(x)), "tern_moe")
+    T, H = x.shape
+    E, F = gate_up.shape[0], down.shape[2] * 4
+    device = x.device
+    _need_at(logits, "logits", device, _FLOATS, (T, E))
+    _need_at(gate_up, "gate_up", device, _U8, (E, 2 * F, H // 4))
+    _need_at(gate_up_scales, "gate_up_scales", device, _F16, (E, 2 * F, H // group))
+    _need_at(down, "down", device, _U8, (E, H, F // 4))
+    _need_at(down_scales, "down_scales", device, _F16, (E, H, F // group))
+    _need_at(out, "out", device, _FLOATS, (T, H))
+    nbytes = lib.tern_moe_workspace(T, E, top_k, H, F)
+    # allocated on the current stream: torch's allocator keeps it for this call until that stream
+    # has passed it, and inside a graph capture it belongs to the graph
+    ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    _launch(lib.tern_moe, "tern_moe", x, x.data_ptr(), _TORCH_CODE[x.dtype], logits.data_ptr(),
+            _TORCH_CODE[logits.dtype], gate_up.data_ptr(), gate_up_scales.data_ptr(), down.data_ptr(),
+            down_scales.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], T, E, top_k, H, F, group,
+            int(renormalize), ws.data_ptr(), nbytes)
     return out
 
 
