@@ -8,24 +8,28 @@
 //
 // Work layout.  A workgroup of WM x WN waves computes BM x BN outputs, BM =
 // 16 MB WM, BN = 16 NB WN.  Per step both operands are staged in LDS as they
-// are stored, double-buffered, one barrier a step: 128 bytes of a row of X
-// (64 or 256 values), and the same K range of a row of W (32 or 128 bytes).
-// The weights stay 4-bit in LDS, so that the fragment reads of a wave are
-// mostly X's; a wave decodes its own fragments (4 instructions for 8 weights,
-// shared by MB matrix instructions).  The loads of step s + 1 go from memory
-// straight to LDS while the products of step s run.
+// are stored: 64 values of a row of X in 128 bytes and the same 64 weights in
+// 32, or 256 4-bit values of either in 128 bytes.  They go from memory straight
+// to LDS, into one of ST buffers, ST - 1 steps before they are needed: every
+// CU misses its XCD's L2 on its first touch of a line, and with two buffers the
+// steps waited for memory (2.3 us a step for 0.6 us of matrix instructions
+// with 4-bit X).  The weights stay 4-bit in LDS, so that the fragment reads of
+// a wave are mostly X's; a wave decodes its own fragments (4 instructions for
+// 8 weights, shared by MB matrix instructions).
 //
 // The rows of the matrix tile are weights and its columns activations: a lane
 // then holds 4 consecutive outputs of one row of Y.  Which K indices share a
-// matrix instruction does not matter as long as both operands agree: lane
-// group p = lane / 16 takes the 16-byte chunks 2 p and 2 p + 1 of a row of X,
-// so that the scale bytes of a lane's two instructions lie side by side.
+// matrix instruction does not matter as long as both operands agree: with
+// 16-bit X lane group p = lane / 16 takes values 16 p .. 16 p + 15 of the 64,
+// half of a block of weights.
 //
-// LDS rows of 128 bytes have their 16-byte chunks XOR-swizzled by (row / 2)
-// mod 8: the 16 lanes of a fragment read fall on 64 distinct banks.
+// LDS rows are XOR-swizzled in 16-byte chunks so that the lanes of a fragment
+// read that are served together fall on distinct banks.
 //
 // Bound: the matrix cores.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "tern_device.h"
 #include "tern_mx.h"
@@ -38,13 +42,23 @@ namespace {
 typedef int int8v_t __attribute__((ext_vector_type(8)));
 typedef float float4v_t __attribute__((ext_vector_type(4)));
 
-constexpr int ROWB = 128;   // bytes of a row of X per step
+// A 16-byte read of the wave is served in groups of lanes such as 0-3, 12-15, 20-27: rows 0-3
+// and 12-15 of one lane group p and 4-11 of the next.  Their 16 chunks have to fall on distinct
+// places of 256 bytes.
+//
+// Rows of 128 bytes, chunks 2 p (+ 1): the row pair h = (row / 2) mod 8, rotated left by a bit,
+// is XORed in (h itself made every read a two-way conflict).
+__device__ __forceinline__ int xor128(int row) { return ((row & 6) | ((row >> 3) & 1)) & 7; }
+// Rows of 32 bytes, read 8 bytes a lane.
+__device__ __forceinline__ int xor32(int row) { return (row >> 3) & 1; }
 
-__device__ __forceinline__ int swz(int r, int c) { return r * ROWB + ((c ^ ((r >> 1) & 7)) << 4); }
+template <int ROWB>
+__device__ __forceinline__ int swz(int row, int c) {
+    return row * ROWB + ((c ^ (ROWB == 128 ? xor128(row) : xor32(row))) << 4);
+}
 
-// 16-bit X: rows of W are 32 bytes per step, two 16-byte blocks; their places
-// alternate every 8 rows, so that the 16 lanes of a read cover all banks.
-__device__ __forceinline__ int wswz(int r, int c) { return r * 32 + ((c ^ ((r >> 3) & 1)) << 4); }
+// Lambdas of the kernel: left as calls, their captures live in scratch memory.
+#define TERN_INLINE __attribute__((always_inline))
 
 constexpr int OUT_OF_RANGE = (int)0x80000000;
 
@@ -57,8 +71,28 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t *lds, i
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, off, at, 0, 0);
 }
 
-// Every load of this wave has arrived (vmcnt 0).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// At most LATER loads of this wave are still on their way, its LDS accesses are done, and every
+// wave of the workgroup has got here.  In one piece: __syncthreads would wait for every load.
+template <int LATER>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER) : "memory");
+}
+
+// The order of a step's LDS reads and matrix instructions: the first operands and AHEAD more
+// fragments of X are read, then a fragment goes out with every NB matrix instructions, so that
+// a read has AHEAD times as long to arrive.  Left to itself the compiler waits for each pair of
+// reads right after it issues them.
+constexpr int AHEAD = 3;
+template <bool MX, int MB, int NB, int TERMS>
+__device__ __forceinline__ void interleave() {
+    constexpr int DS = 0x100, MFMA = 0x008;
+    __builtin_amdgcn_sched_group_barrier(DS, (MX ? MB + 3 * NB : 2 * NB) + AHEAD, 0);
+#pragma unroll
+    for (int g = 0; g < 2 * MB; ++g) {
+        __builtin_amdgcn_sched_group_barrier(MFMA, NB * TERMS, 0);
+        __builtin_amdgcn_sched_group_barrier(DS, 1, 0);
+    }
+}
 
 // 32 4-bit values as the operand of a matrix instruction.
 __device__ __forceinline__ int8v_t quarter(const uint8_t *at) {
@@ -66,102 +100,139 @@ __device__ __forceinline__ int8v_t quarter(const uint8_t *at) {
     return (int8v_t){(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
 }
 
-template <int XT, int WM, int WN, int MB, int NB>
+template <int XT, int WM, int WN, int MB, int NB, int ST>
 struct Shape {
     static constexpr bool MX = XT == 2;
-    static constexpr int NT = 64 * WM * WN;
+    static constexpr int WAVES = WM * WN, NT = 64 * WAVES;
     static constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN;
     static constexpr int BPS = MX ? 8 : 2;            // blocks of 32 per step
-    static constexpr int WROW = MX ? 128 : 32;        // bytes of a row of W per step
-    static constexpr int WAVES = WM * WN;
-    static constexpr int A_LDS = BM * ROWB, W_LDS = BN * WROW;
-    static constexpr int AI = A_LDS / 1024 / WAVES;                      // load instructions per wave
+    static constexpr int XROW = 128;                  // bytes of a row of X per step
+    static constexpr int WROW = MX ? 128 : 32;        // and of W
+    static constexpr int A_LDS = BM * XROW, W_LDS = BN * WROW;
+    static constexpr int AI = (A_LDS / 1024 + WAVES - 1) / WAVES;        // load instructions per wave
     static constexpr int WI = (W_LDS / 1024 + WAVES - 1) / WAVES;
     static constexpr int SROWS = MX ? BM + BN : BN;                      // rows with scale bytes
     static constexpr int SP = (SROWS + NT - 1) / NT;
-    static constexpr int BUF = A_LDS + W_LDS + SROWS * BPS;
+    static constexpr int S_AT = (AI + WI) * WAVES * 1024;                // where they start
+    static constexpr int BUF = S_AT + SP * NT * BPS;                     // every thread stores SP rows, no branch
+    static constexpr int CH = 16 / BPS;                                  // steps per 16 scale bytes of a row
+    static constexpr int LOADS = AI + WI;                                // tile loads of a wave per step
     static_assert(A_LDS % (1024 * WAVES) == 0 && W_LDS % 1024 == 0, "whole load instructions");
-    static_assert(WAVES % 2 == 0, "a lane's swizzle must not depend on the instruction");
+    static_assert(ST >= 2 && ST <= 4 && ST * BUF <= 160 * 1024, "buffers");
+    static_assert(ST - 1 <= CH, "the first steps' scales come from one chunk");
+    static_assert((ST - 2) * LOADS < 64, "the wait counter has 6 bits");
 };
 
-template <int XT, int WM, int WN, int MB, int NB>
+template <int XT, int WM, int WN, int MB, int NB, int ST>
 __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__restrict__ X,
                                                              const uint8_t *__restrict__ XE,
                                                              const uint8_t *__restrict__ W,
                                                              const uint8_t *__restrict__ WE, void *__restrict__ Y,
                                                              int y_dtype, int M, int N, int blocks, int tiles_m,
                                                              int tiles_n, int vec) {
-    typedef Shape<XT, WM, WN, MB, NB> T;
-    // two variables, so that the compiler sees that the reads of one need not wait for the loads into the other
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[T::BUF];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[T::BUF];
+    typedef Shape<XT, WM, WN, MB, NB, ST> T;
+    // One variable each, so that the compiler sees that an access to one need not wait for the loads
+    // into another.
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[T::BUF], buf1[T::BUF];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[ST > 2 ? T::BUF : 16], buf3[ST > 3 ? T::BUF : 16];
+    auto buf = [&](auto i) TERN_INLINE {
+        constexpr int I = decltype(i)::value % ST;
+        if constexpr (I == 0) return buf0;
+        else if constexpr (I == 1) return buf1;
+        else if constexpr (I == 2) return buf2;
+        else return buf3;
+    };
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int p = lane >> 4, li = lane & 15;
 
-    // Each XCD takes a contiguous run of tiles (workgroups go round the 8 XCDs).
+    // Workgroups go round the 8 XCDs: each XCD gets a contiguous run of tiles, which goes down
+    // bands of 8 tile rows, so that its 32 CUs share 8 row tiles and 4 column tiles in its L2.
     const int ntiles = tiles_m * tiles_n;
     int tile = blockIdx.x;
     if (ntiles % 8 == 0) tile = (blockIdx.x % 8) * (ntiles / 8) + blockIdx.x / 8;
-    const int m0 = tile / tiles_n * T::BM, n0 = tile % tiles_n * T::BN;
+    const int band = tile / (8 * tiles_n), in = tile - band * 8 * tiles_n, bandm = min(8, tiles_m - band * 8);
+    const int m0 = (band * 8 + in % bandm) * T::BM, n0 = in / bandm * T::BN;
 
     const int xrow = blocks * (T::MX ? 16 : 64), wrow = blocks * 16;
     const int xrows = min(T::BM, M - m0), wrows = min(T::BN, N - n0);
     const __amdgpu_buffer_rsrc_t rx = rows_of(X + (int64_t)m0 * xrow, xrows * xrow);
     const __amdgpu_buffer_rsrc_t rw = rows_of(W + (int64_t)n0 * wrow, wrows * wrow);
-    const uint8_t *xeb = T::MX ? XE + (int64_t)m0 * blocks : nullptr, *web = WE + (int64_t)n0 * blocks;
     const int steps = (blocks + T::BPS - 1) / T::BPS;
 
-    // Tiles go from memory straight to LDS, 16 bytes a lane, 1 KB an instruction: 8 rows of 128
-    // bytes, or 32 rows of 32.  Rows past the end, and in the last step the chunks past the end
-    // of a row, get an offset out of range and arrive as zeros.
-    const int ac = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));   // this lane's chunk (swz)
-    const int wc = T::MX ? ac : (lane & 1) ^ ((lane >> 4) & 1);      // (wswz)
-    const int aoff = (wave * 8 + (lane >> 3)) * xrow + ac * 16;
-    const int woff = (T::MX ? wave * 8 + (lane >> 3) : wave * 32 + (lane >> 1)) * wrow + wc * 16;
-    auto fetch = [&](uint8_t *buf, int s) {
+    // Tiles go from memory straight to LDS, 16 bytes a lane, 1 KB an instruction.  Rows past the
+    // end, chunks past the end of a row in the last step, and instructions past the tile (every
+    // wave issues as many) get an offset out of range and arrive as zeros.
+    constexpr int XL = T::XROW / 16, WL = T::WROW / 16;   // lanes per row
+    const int ar = wave * (64 / XL) + lane / XL, wr = wave * (64 / WL) + lane / WL;
+    const int ac = (lane % XL) ^ xor128(ar);
+    const int wc = (lane % WL) ^ (T::MX ? xor128(wr) : xor32(wr));
+    const int aoff = ar * xrow + ac * 16, woff = wr * wrow + wc * 16;
+    auto fetch = [&](uint8_t *to, int s) TERN_INLINE {
         const int left = blocks - s * T::BPS;   // blocks of this step
         const int ao = ac < left * (T::MX ? 1 : 4) ? aoff : OUT_OF_RANGE;
         const int wo = wc < left ? woff : OUT_OF_RANGE;
 #pragma unroll
         for (int i = 0; i < T::AI; ++i)
-            to_lds(rx, buf + (i * T::WAVES + wave) * 1024, ao, i * T::WAVES * 8 * xrow + s * ROWB);
+            to_lds(rx, to + (i * T::WAVES + wave) * 1024, ao, i * T::WAVES * (64 / XL) * xrow + s * T::XROW);
 #pragma unroll
         for (int i = 0; i < T::WI; ++i)
-            if (T::W_LDS / 1024 % T::WAVES == 0 || i * T::WAVES + wave < T::W_LDS / 1024)
-                to_lds(rw, buf + T::A_LDS + (i * T::WAVES + wave) * 1024, wo,
-                       i * T::WAVES * (T::MX ? 8 : 32) * wrow + s * T::WROW);
+            to_lds(rw, to + T::A_LDS + (i * T::WAVES + wave) * 1024, wo,
+                   i * T::WAVES * (64 / WL) * wrow + s * T::WROW);
     };
 
-    // Scale bytes go through registers (rows of blocks bytes have no alignment).  Places past the
-    // end get 127, the scale 1: a stray 255 would make NaN of the zeros there.
-    uint64_t sr[T::SP];
-    auto load_scales = [&](int s) {
-        const int left = blocks - s * T::BPS;
+    // Scale bytes go through registers, 16 of a row at a time (512 values): a load costs a request
+    // to the L2 per row however short it is, and 4 bytes a step were as many requests as the tiles
+    // themselves.  A step's bytes are stored just before its tiles are fetched into the same buffer.
+    // Places past the end of a row get 127, the scale 1: a stray 255 would make NaN of the zeros
+    // there.  Rows have no alignment; a load that would pass the end of the matrix starts earlier and
+    // is shifted when it is taken (a matrix has at least 16 scale bytes).
+    uint4 scur[T::SP], snext[T::SP];
+    const uint8_t *srow[T::SP];   // the row's scale bytes
+    int slast[T::SP];             // the last place in it that 16 bytes can be loaded from
 #pragma unroll
-        for (int i = 0; i < T::SP; ++i) {
-            const int r = i * T::NT + tid;
-            const uint8_t *e = T::MX && r < T::BM ? xeb + (int64_t)min(r, xrows - 1) * blocks
-                                                  : web + (int64_t)min(r - (T::MX ? T::BM : 0), wrows - 1) * blocks;
-            e += s * T::BPS;
-            if (left >= T::BPS) {
-                sr[i] = 0;
-                __builtin_memcpy(&sr[i], e, T::BPS);
-            } else {
-                sr[i] = 0x7F7F7F7F7F7F7F7Full;
-                for (int b = 0; b < left; ++b) sr[i] ^= (uint64_t)(e[b] ^ 127) << (8 * b);
-            }
+    for (int i = 0; i < T::SP; ++i) {
+        const int r = i * T::NT + tid;
+        if (T::MX && r < T::BM) {
+            const int64_t row = m0 + min(r, xrows - 1);
+            srow[i] = XE + row * blocks;
+            slast[i] = (int)min((M - row) * blocks - 16, (int64_t)1 << 30);
+        } else {
+            const int64_t row = n0 + min(r - (T::MX ? T::BM : 0), wrows - 1);
+            srow[i] = WE + row * blocks;
+            slast[i] = (int)min((N - row) * blocks - 16, (int64_t)1 << 30);
         }
+    }
+    auto load_scales = [&](int q) TERN_INLINE {
+#pragma unroll
+        for (int i = 0; i < T::SP; ++i) __builtin_memcpy(&snext[i], srow[i] + min(q * 16, slast[i]), 16);
     };
-    auto store_scales = [&](uint8_t *buf) {
-        uint8_t *sc = buf + T::A_LDS + T::W_LDS;
+    auto take_scales = [&](int q) TERN_INLINE {   // chunk q becomes the current one, q + 1 goes out
 #pragma unroll
         for (int i = 0; i < T::SP; ++i) {
+            const int sh = 8 * min(max(q * 16 - slast[i], 0), 15);
+            uint64_t lo = snext[i].x | (uint64_t)snext[i].y << 32, hi = snext[i].z | (uint64_t)snext[i].w << 32;
+            if (sh >= 64) lo = hi, hi = 0;
+            if (sh & 63) lo = lo >> (sh & 63) | hi << (64 - (sh & 63)), hi >>= sh & 63;
+            scur[i] = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+        }
+        load_scales(q + 1);
+    };
+    auto store_scales = [&](uint8_t *to, int s) TERN_INLINE {
+        const int left = min(max(blocks - s * T::BPS, 0), T::BPS);
+        const uint64_t valid = left == 8 ? ~0ull : (1ull << (8 * left)) - 1;
+        const int at = s % T::CH;   // its place in the chunk
+#pragma unroll
+        for (int i = 0; i < T::SP; ++i) {
+            const uint4 &c = scur[i];
             const int r = i * T::NT + tid;
-            if (T::SROWS % T::NT == 0 || r < T::SROWS) {
-                if constexpr (T::MX) *reinterpret_cast<uint64_t *>(sc + r * 8) = sr[i];
-                else *reinterpret_cast<uint16_t *>(sc + r * 2) = (uint16_t)sr[i];
+            if constexpr (T::MX) {
+                const uint64_t v = at ? c.z | (uint64_t)c.w << 32 : c.x | (uint64_t)c.y << 32;
+                *reinterpret_cast<uint64_t *>(to + T::S_AT + r * 8) = (v & valid) | (0x7F7F7F7F7F7F7F7Full & ~valid);
+            } else {
+                const uint32_t v = (at < 2 ? c.x : at < 4 ? c.y : at < 6 ? c.z : c.w) >> 16 * (at & 1);
+                *reinterpret_cast<uint16_t *>(to + T::S_AT + r * 2) = (uint16_t)((v & valid) | (0x7F7Fu & ~valid));
             }
         }
     };
@@ -173,49 +244,49 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
         for (int m = 0; m < MB; ++m) acc[n][m] = (float4v_t){0.f, 0.f, 0.f, 0.f};
 
     const int arow = wm * 16 * MB + li, wrow0 = wn * 16 * NB + li;
-    auto products = [&](const uint8_t *a) {
-        const uint8_t *w = a + T::A_LDS, *sc = w + T::W_LDS;
+    auto products = [&](const uint8_t *a) TERN_INLINE {
+        const uint8_t *w = a + T::A_LDS;
+        const uint8_t *sc = a + T::S_AT;
         if constexpr (T::MX) {
-            uint32_t as[MB], bs[NB];
+            uint32_t as[MB], bs[NB];   // two scale bytes each
+            int8v_t bv[2][NB];
 #pragma unroll
             for (int m = 0; m < MB; ++m) as[m] = *reinterpret_cast<const uint16_t *>(sc + (arow + 16 * m) * 8 + 2 * p);
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n) {
                 bs[n] = *reinterpret_cast<const uint16_t *>(sc + (T::BM + wrow0 + 16 * n) * 8 + 2 * p);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                int8v_t bv[NB];
+                for (int j = 0; j < 2; ++j) bv[j][n] = quarter(w + swz<T::WROW>(wrow0 + 16 * n, 2 * p + j));
+            }
 #pragma unroll
-                for (int n = 0; n < NB; ++n) bv[n] = quarter(w + swz(wrow0 + 16 * n, 2 * p + j));
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
-                    const int8v_t av = quarter(a + swz(arow + 16 * m, 2 * p + j));
+                    const int8v_t av = quarter(a + swz<T::XROW>(arow + 16 * m, 2 * p + j));
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
                         // the byte selects are immediates
                         if (j == 0)
-                            acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[n], av, acc[n][m], 4, 4, 0,
+                            acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[0][n], av, acc[n][m], 4, 4, 0,
                                                                                          (int)bs[n], 0, (int)as[m]);
                         else
-                            acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[n], av, acc[n][m], 4, 4, 1,
+                            acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[1][n], av, acc[n][m], 4, 4, 1,
                                                                                          (int)bs[n], 1, (int)as[m]);
                     }
                 }
-                if (j == 0) __builtin_amdgcn_sched_barrier(0);
-            }
         } else {
             uint2 code[NB];
             float sf[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                code[n] = *reinterpret_cast<const uint2 *>(w + wswz(wrow0 + 16 * n, p >> 1) + 8 * (p & 1));
+                code[n] = *reinterpret_cast<const uint2 *>(w + swz<T::WROW>(wrow0 + 16 * n, p >> 1) + 8 * (p & 1));
                 sf[n] = __builtin_bit_cast(float, (uint32_t)sc[(wrow0 + 16 * n) * 2 + (p >> 1)] << 23);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint4 xv[MB];
 #pragma unroll
-                for (int m = 0; m < MB; ++m) xv[m] = *reinterpret_cast<const uint4 *>(a + swz(arow + 16 * m, 2 * p + i));
+                for (int m = 0; m < MB; ++m) xv[m] = *reinterpret_cast<const uint4 *>(a + swz<T::XROW>(arow + 16 * m, 2 * p + i));
                 bf168_t bv[NB];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) bv[n] = decode8(i ? code[n].y : code[n].x, sf[n]);
@@ -236,28 +307,47 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
         }
     };
 
-    // One step: the products of `now` while `next` fills.
-    auto step = [&](uint8_t *now, uint8_t *next, int s) {
-        const bool more = s + 1 < steps;
-        if (more) {
-            fetch(next, s + 1);
-            load_scales(s + 1);
-        }
-        products(now);
-        if (more) store_scales(next);
-        wait_loads();
-        __syncthreads();
+    // Step s, in buffer I = s mod ST, fetches step s + ST - 1.  Past the end every offset is out of
+    // range; a branch around the fetch would let the compiler move the products behind the wait.
+    auto step = [&](auto i, int s) TERN_INLINE {
+        constexpr int I = decltype(i)::value;
+        constexpr auto fill = std::integral_constant<int, (I + ST - 1) % ST>();
+        const int f = s + ST - 1;
+        if (ST == T::CH ? fill.value == 0 : f % T::CH == 0) take_scales(f / T::CH);
+        store_scales(buf(fill), f);
+        fetch(buf(fill), f);
+        __builtin_amdgcn_sched_barrier(0);   // the loads first
+        products(buf(i));
+        interleave<T::MX, MB, NB, XT == 0 ? 2 : 1>();
+        __builtin_amdgcn_sched_barrier(0);   // and the wait last
+        wait_and_meet<(ST - 2) * T::LOADS>();   // step s + 1 is there
     };
-    fetch(buf0, 0);
+    auto each = [&](auto f) TERN_INLINE {   // f(0), ..., f(ST - 1) until one returns true
+        typedef std::integral_constant<int, 0> I0;
+        typedef std::integral_constant<int, 1> I1;
+        if (f(I0()) || f(I1())) return true;
+        if constexpr (ST > 2)
+            if (f(std::integral_constant<int, 2>())) return true;
+        if constexpr (ST > 3)
+            if (f(std::integral_constant<int, 3>())) return true;
+        return false;
+    };
     load_scales(0);
-    store_scales(buf0);
-    wait_loads();
-    __syncthreads();
-    for (int s = 0;;) {
-        step(buf0, buf1, s);
-        if (++s >= steps) break;
-        step(buf1, buf0, s);
-        if (++s >= steps) break;
+    take_scales(0);
+    each([&](auto i) TERN_INLINE {
+        constexpr int I = decltype(i)::value;
+        if constexpr (I < ST - 1) {
+            store_scales(buf(i), I);
+            fetch(buf(i), I);
+        }
+        return false;
+    });
+    wait_and_meet<0>();
+    int s = 0;
+    while (!each([&](auto i) TERN_INLINE {
+        step(i, s);
+        return ++s >= steps;
+    })) {
     }
 
     // lane (p, li): outputs n = 4 p + v of row li of each 16 x 16 block
@@ -292,10 +382,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
         }
 }
 
-template <int XT, int WM, int WN, int MB, int NB>
+template <int XT, int WM, int WN, int MB, int NB, int ST>
 hipError_t launch_t(const MxArgs &a) {
-    typedef Shape<XT, WM, WN, MB, NB> T;
-    constexpr auto kern = &mx_gemm_kernel<XT, WM, WN, MB, NB>;
+    typedef Shape<XT, WM, WN, MB, NB, ST> T;
+    constexpr auto kern = &mx_gemm_kernel<XT, WM, WN, MB, NB, ST>;
     const int tm = (int)((a.M + T::BM - 1) / T::BM), tn = (int)((a.N + T::BN - 1) / T::BN);
     const size_t unit = a.y_dtype == 2 ? 16 : 8;
     const int vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % unit == 0;
@@ -307,17 +397,19 @@ hipError_t launch_t(const MxArgs &a) {
 template <int XT>
 hipError_t launch_x(const MxArgs &a) {
     if (a.M > 128) {
-        if constexpr (XT == 2) return launch_t<XT, 2, 4, 8, 4>(a);
-        else return launch_t<XT, 2, 4, 8, 4>(a);   // 256 x 256
+        if constexpr (XT == 2) return launch_t<XT, 2, 4, 8, 3, 2>(a);
+        else return launch_t<XT, 2, 4, 8, 4, 3>(a);   // 256 x 256
     }
-    return launch_t<XT, 2, 2, 2, 4>(a);                  // 64 x 128
+    if constexpr (XT == 2) return launch_t<XT, 2, 2, 2, 4, 2>(a);                  // 64 x 128
+    else return launch_t<XT, 2, 2, 2, 4, 4>(a);
 }
 
 }  // namespace
 
-// Offsets inside a tile are 32-bit, tiles are counted in an int.
+// Scale bytes are loaded 16 at a time, offsets inside a tile are 32-bit, tiles are counted in an int.
 bool mx_gemm_fits(const MxArgs &a) {
-    return a.K <= (1 << 21) && ((a.M + 63) / 64) * ((a.N + 63) / 64) < (int64_t(1) << 31);
+    const int64_t blocks = a.K / 32;
+    return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) && ((a.M + 63) / 64) * ((a.N + 63) / 64) < (int64_t(1) << 31);
 }
 
 hipError_t launch_mx_gemm(const MxArgs &a) {
