@@ -119,6 +119,7 @@ struct Shape {
     static constexpr int LOADS = AI + WI;                                // tile loads of a wave per step
     static_assert(A_LDS % (1024 * WAVES) == 0 && W_LDS % 1024 == 0, "whole load instructions");
     static_assert(ST >= 2 && ST <= 4 && ST * BUF <= 160 * 1024, "buffers");
+    static_assert(!MX || (ST == 2 && BM / 4 <= 64 && BN / 8 <= 64), "touched lines: one instruction, waited for in its step");
     static_assert(ST - 1 <= CH, "the first steps' scales come from one chunk");
     static_assert((ST - 2) * LOADS < 64, "the wait counter has 6 bits");
 };
@@ -135,6 +136,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
     // into another.
     __shared__ __attribute__((aligned(16))) uint8_t buf0[T::BUF], buf1[T::BUF];
     __shared__ __attribute__((aligned(16))) uint8_t buf2[ST > 2 ? T::BUF : 16], buf3[ST > 3 ? T::BUF : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t touched[T::MX ? 512 : 16];   // written, never read
     auto buf = [&](auto i) TERN_INLINE {
         constexpr int I = decltype(i)::value % ST;
         if constexpr (I == 0) return buf0;
@@ -180,6 +182,20 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
         for (int i = 0; i < T::WI; ++i)
             to_lds(rw, to + T::A_LDS + (i * T::WAVES + wave) * 1024, wo,
                    i * T::WAVES * (64 / WL) * wrow + s * T::WROW);
+    };
+
+    // With 4-bit X a step is short and its tiles come late: every line is new to the XCD's L2.  So
+    // the lines of one step further are touched (4 bytes each, into a corner of LDS), every CU its
+    // share of what the band's CUs read together: 4 of them a row tile, 8 a column tile.  Measured
+    // at M = 2048, 5120 -> 17408: 140 -> 129 us; with 16-bit X, whose steps are longer, 158 -> 164.
+    const bool tx = wave == 0;
+    const __amdgpu_buffer_rsrc_t rt = tx ? rx : rw;
+    const int tshare = tx ? in / bandm % 4 * (T::BM / 4) : in % bandm * (T::BN / 8);
+    const int toff = lane < (tx ? T::BM / 4 : T::BN / 8) ? (tshare + lane) * (tx ? xrow : wrow) : OUT_OF_RANGE;
+    auto touch = [&](int s) TERN_INLINE {
+        if (T::MX && wave < 2 && s < steps)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rt, (__attribute__((address_space(3))) void *)(touched + wave * 256), 4, toff, s * T::XROW, 0, 0);
     };
 
     // Scale bytes go through registers, 16 of a row at a time (512 values): a load costs a request
@@ -314,6 +330,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
         constexpr auto fill = std::integral_constant<int, (I + ST - 1) % ST>();
         const int f = s + ST - 1;
         if (ST == T::CH ? fill.value == 0 : f % T::CH == 0) take_scales(f / T::CH);
+        touch(f + 1);
         store_scales(buf(fill), f);
         fetch(buf(fill), f);
         __builtin_amdgcn_sched_barrier(0);   // the loads first
