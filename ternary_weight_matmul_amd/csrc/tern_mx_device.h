@@ -18,21 +18,25 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// bf16 hi (term 0) or lo (term 1) of 8 fp16 values.  hi + lo is the value
-// exactly: hi keeps 8 of its 11 significant bits and lo the rest.  An
-// infinity would leave inf - inf in lo: its lo is 0.
-__device__ __forceinline__ uint4 fp16_term(const uint4 &q, bool lo) {
+// The two bf16 terms of 8 fp16 values, hi (returned) and lo.  hi is the value
+// without its last 3 significant bits, lo those bits: hi + lo is the value
+// exactly.  (An infinity has the lo inf - inf, NaN.)
+__device__ __forceinline__ uint4 fp16_terms(const uint4 &q, uint4 &lo) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t o[4];
+    uint32_t h[4], l[4];
+    // the upper halves of two fp32: exact, both terms have 8 significant bits at most
+    auto pair = [](half2_t v) {
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, (float)v[1]), __builtin_bit_cast(uint32_t, (float)v[0]),
+                                     0x07060302u);
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = f16_bits_to_float((uint16_t)w[i]), b = f16_bits_to_float((uint16_t)(w[i] >> 16));
-        const uint32_t hi = bf16_pair(a, b);
-        const float ah = __builtin_bit_cast(float, hi << 16), bh = __builtin_bit_cast(float, hi & 0xFFFF0000u);
-        const uint32_t rest = bf16_pair(a == ah ? 0.f : a - ah, b == bh ? 0.f : b - bh);
-        o[i] = lo ? rest : hi;
+        const half2_t v = __builtin_bit_cast(half2_t, w[i]), t = __builtin_bit_cast(half2_t, w[i] & 0xFFF8FFF8u);
+        h[i] = pair(t);
+        l[i] = pair(v - t);
     }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+    return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // 8 e2m1 codes -> 8 bf16 values times the scale s (exact: two significant bits).

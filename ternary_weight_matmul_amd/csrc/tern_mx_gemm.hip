@@ -308,15 +308,17 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
                 for (int n = 0; n < NB; ++n) bv[n] = decode8(i ? code[n].y : code[n].x, sf[n]);
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
-                    const bf168_t hi = __builtin_bit_cast(bf168_t, XT == 0 ? fp16_term(xv[m], false) : xv[m]);
+                    uint4 lo;
+                    const uint4 hi = XT == 0 ? fp16_terms(xv[m], lo) : xv[m];
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
-                        acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], hi, acc[n][m], 0, 0, 0);
+                        acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], __builtin_bit_cast(bf168_t, hi),
+                                                                           acc[n][m], 0, 0, 0);
                     if constexpr (XT == 0) {
-                        const bf168_t lo = __builtin_bit_cast(bf168_t, fp16_term(xv[m], true));
 #pragma unroll
                         for (int n = 0; n < NB; ++n)
-                            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], lo, acc[n][m], 0, 0, 0);
+                            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], __builtin_bit_cast(bf168_t, lo),
+                                                                               acc[n][m], 0, 0, 0);
                     }
                 }
             }
