@@ -275,7 +275,8 @@ tern_status tern_mx_matmul_mx(const uint8_t *x_codes, const uint8_t *x_exps, con
  *       F..2F-1 Wu; gate_up_scales [E,2F,H/128] fp16
  *   down [E,H,F/4], down_scales [E,H,F/128]: Wd
  *   group must be 128 and divide H and F; 1 <= top_k <= min(E, 32) and
- *   E <= 1024 (TERN_ERR_UNSUPPORTED beyond those two limits).
+ *   E <= 1024 (TERN_ERR_UNSUPPORTED beyond those two limits); H, F <= 16384
+ *   (TERN_ERR_SHAPE: the tokens of an expert stay in LDS).
  *   workspace: tern_moe_workspace bytes (TERN_ERR_SHAPE if fewer), 256-byte
  *       aligned, for this call alone until the stream has passed it.
  * Hidden values and all sums are fp32; Y is rounded once.  Any T; tokens are

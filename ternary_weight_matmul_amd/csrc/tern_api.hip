@@ -201,10 +201,9 @@ tern_status mx_product(const void *X, const uint8_t *XE, int x_dtype, const uint
 
 bool moe_sizes_ok(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {
     if (T < 0 || E < 0 || top_k < 0 || H < 0 || F < 0) return false;
-    if (T > kMaxDim || E > kMaxDim || top_k > kMaxDim || H > kMaxK || F > kMaxK) return false;
-    // 2 E F H weights, T H and T E values, pairs * (F + H) floats of workspace
-    return product_ok(H, F) && product_ok(2 * E, H * F) && product_ok(T, H) && product_ok(T, E) &&
-           product_ok(top_k, (H + F) * tern::kMoeChunk * 8);
+    if (T > kMaxDim || E > kMaxDim || top_k > kMaxDim || H > tern::kMoeMaxWidth || F > tern::kMoeMaxWidth)
+        return false;
+    return product_ok(2 * E, H * F) && product_ok(T, H) && product_ok(T, E);   // weights, values, logits
 }
 
 }  // namespace

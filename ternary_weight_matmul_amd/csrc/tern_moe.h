@@ -11,6 +11,8 @@ namespace tern {
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
 constexpr int64_t kMoeChunk = 64;   // tokens of one pass over the experts
+constexpr int kMoeSmall = 4;        // tokens up to which two launches do
+constexpr int64_t kMoeMaxWidth = 16384;   // H and F: four tokens' operands stay in LDS
 
 struct MoeArgs {
     const void *X;               // [T,H] fp16/bf16

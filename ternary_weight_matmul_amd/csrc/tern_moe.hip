@@ -8,22 +8,43 @@
 //   h[e] = silu(Wg[e] x) * (Wu[e] x),  y = sum over e in S of w[e] Wd[e] h[e]
 // with ternary Wg, Wu (the two halves of gate_up) and Wd.  The weights become
 // +-2 / 0 operands (tern_device.h) of the 16-bit matrix instructions, a
-// 128-weight block's fp32 sum is multiplied by its fp16 scale.  The hidden
-// values stay fp32 and enter the down product as two bf16 terms, hi = bf16(h)
-// and lo = bf16(h - hi): 16 significant bits, so that this product adds no
-// rounding that a 16-bit output would show.
+// 128-weight block's fp32 sum is multiplied by its fp16 scale.  w h is handed
+// to the down product as two bf16 terms, hi = bf16(w h) and lo = bf16(w h - hi):
+// 16 significant bits, so that this product adds no rounding that a 16-bit
+// output would show.
 //
-// Work layout of both products.  Waves of a workgroup split K into 512-weight
-// steps.  Lane (p = lane / 16, col = 4 r + c) loads the 8 code bytes of slice
-// p of block c of row r of a 4-row quad: one instruction reads 4 rows x 128
-// contiguous bytes.  Tile row i = 4 c' + s holds activation slot s in block c',
-// so that only the results with c' = c are used, each with its own scale.
+// Launches.  Up to kMoeSmall tokens take two: the up kernel, whose workgroups
+// each route every token anew (a microsecond, against two for a launch of its
+// own), and a down kernel whose workgroups own output rows, go through all
+// taken experts and sum in registers.  More tokens take four: routing and the
+// list of each expert's tokens, up, down with a partial output per (token,
+// choice), and the sum of a token's partials.
 //
-// Bound: HBM (the codes of the experts that are taken, once for all of their
-// tokens).
+// Work layout of up and down.  A workgroup works for one expert: it holds the
+// activations of the expert's tokens in LDS, as the matrix instructions take
+// them, and each wave takes units of Q quads of weight rows over all of K.
+// Lane (p = lane / 16, col = 4 r + c) loads the 8 code bytes of slice p of
+// block c of row r of a quad: one instruction reads 4 rows x 128 contiguous
+// bytes.  Tile row i = 4 c' + s holds activation slot s in block c', so that
+// only the results with c' = c are used, each with its own scale.  A quad's
+// loads are refilled, G steps of 512 weights ahead, as soon as it is used; the
+// first are on their way before the activations are fetched.
+//   With K split over the waves instead, sums met in LDS once a block of rows,
+// each behind a barrier: 107 us for both products at 32 tokens of the sizes
+// below, against 62.
+//
+// Bound: HBM for one token (the codes of the experts that are taken, once for
+// all of their tokens: E = 64, k = 8, 2048 x 1024: 12.6 MB, 14 us with both
+// launches, of which routing, first loads and launches are about 8).  At 32
+// tokens (97 MB) decoding the codes, 36 vector instructions a quad and step,
+// and the 8 matrix instructions they feed: 33 + 29 us, and 7 + 5 for the plan
+// and the sum.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "tern_device.h"
+#include "tern_launch.h"
 #include "tern_moe.h"
 
 namespace tern {
@@ -34,8 +55,20 @@ typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4v_t __attribute__((ext_vector_type(4)));
 
-constexpr int E_STEP = 512;
-constexpr int E_MAX_WAVES = 16;
+constexpr int OUT_OF_RANGE = (int)0x80000000;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
+}
+
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, int off, int at) {
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, at, 0)));
+}
+
+// What every lane holds, in a scalar register: a buffer descriptor made from anything else is
+// gathered lane by lane in a loop around each load.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ---- routing ------------------------------------------------------------------
 
@@ -45,145 +78,175 @@ __device__ __forceinline__ float load_logit(const void *l, int dtype, int64_t i)
     return f16_bits_to_float(static_cast<const uint16_t *>(l)[i]);
 }
 
-// Unsigned key in the order of the values: NaN above all, -0 equal to 0.
+// Unsigned key in the order of the values, never 0: NaN above all, -0 equal to 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __builtin_bit_cast(uint32_t, v != v ? __builtin_bit_cast(float, 0x7FC00000u) : v + 0.0f);
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __builtin_bit_cast(float, (k >> 31) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// One wave routes one token: lane j < top_k returns the j-th expert and its
-// weight (-1 and 0 where there is none).
-__device__ void route_token(const void *logits, int l_dtype, int64_t row, int E, int top_k, bool renorm, int lane,
-                            int &id, float &weight) {
-    const int64_t base = row * E;
-    id = -1;
-    float mine = 0.f;       // logit of this lane's choice
-    uint64_t last = ~0ull;  // key of the choice before
-    float top = 0.f;
-    for (int j = 0; j < top_k; ++j) {
-        // the largest (value, lowest index) key below the last one taken
-        uint64_t best = 0;
-        for (int e = lane; e < E; e += 64) {
-            const uint64_t k = ((uint64_t)order_key(load_logit(logits, l_dtype, base + e)) << 32) | (uint32_t)(~e);
-            if (k < last && k > best) best = k;
-        }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+
+// Maximum over the wave, the same for every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, dpp<0x128>(v));   // rotations within rows of 16
+    v = max(v, dpp<0x124>(v));
+    v = max(v, dpp<0x122>(v));
+    v = max(v, dpp<0x121>(v));
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    v = row16_sum(v);
+    auto lane_of = [&](int l) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+    };
+    return (lane_of(0) + lane_of(16)) + (lane_of(32) + lane_of(48));
+}
+
+// One wave routes one token: lane j < top_k gets the j-th expert and its
+// weight (-1 and 0 where there is none).  E <= 64 R.
+template <int R>
+__device__ __forceinline__ void route_token(const void *logits, int l_dtype, int64_t row, int E, int top_k, bool renorm,
+                                            int lane, int &id, float &weight) {
+    uint32_t key[R], all[R];
 #pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) {
-            const uint64_t o = __shfl_xor((unsigned long long)best, m);
-            best = o > best ? o : best;
-        }
-        last = best;
-        const int e = (int)~(uint32_t)best;
-        const float v = load_logit(logits, l_dtype, base + e);
-        if (j == 0) top = v;
-        if (lane == j) {
-            id = v == -__builtin_inff() ? -1 : e;
-            mine = v;
-        }
+    for (int i = 0; i < R; ++i) {
+        const int e = 64 * i + lane;
+        const float v = load_logit(logits, l_dtype, row * E + min(e, E - 1));
+        all[i] = key[i] = e < E ? order_key(v) : 0u;
     }
-    float part;
+    id = -1;
+    uint32_t mine = 0, top = 0;
+    for (int j = 0; j < top_k; ++j) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int i = 1; i < R; ++i) m = max(m, key[i]);
+        m = wave_max(m);
+        if (j == 0) top = m;
+        int e = -1;   // the lowest index that holds it
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const uint64_t hit = __ballot(key[i] == m);
+            if (e < 0 && hit != 0) {
+                e = 64 * i + __ffsll((unsigned long long)hit) - 1;
+                if (lane == (e & 63)) key[i] = 0;
+            }
+        }
+        if (lane == j) id = e, mine = m;
+    }
+    const float t = key_value(top), v = key_value(mine), ninf = -__builtin_inff();
+    if (lane >= top_k || v == ninf) id = -1;
+    float part = 0.f;
     if (renorm) {
-        part = lane < top_k && id >= 0 ? expf(mine - top) : 0.f;
+        if (id >= 0) part = expf(v - t);
     } else {
-        part = 0.f;
-        for (int e = lane; e < E; e += 64) {
-            const float v = load_logit(logits, l_dtype, base + e);
-            if (v != -__builtin_inff()) part += expf(v - top);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float l = key_value(all[i]);
+            if (all[i] != 0 && l != ninf) part += expf(l - t);
         }
     }
     const float total = wave_sum(part);
-    weight = id >= 0 ? expf(mine - top) / total : 0.f;
+    weight = id >= 0 ? expf(v - t) / total : 0.f;
 }
 
-__global__ __launch_bounds__(64) void moe_route_kernel(const void *__restrict__ logits, int l_dtype, int E, int top_k,
-                                                       int renorm, int *__restrict__ ids, float *__restrict__ weights) {
-    const int lane = threadIdx.x;
-    int id;
-    float w;
-    route_token(logits, l_dtype, blockIdx.x, E, top_k, renorm != 0, lane, id, w);
-    if (lane < top_k) {
-        ids[blockIdx.x * top_k + lane] = id;
-        weights[blockIdx.x * top_k + lane] = w;
-    }
+__device__ __forceinline__ void route_any(const void *logits, int l_dtype, int64_t row, int E, int top_k, bool renorm,
+                                          int lane, int &id, float &weight) {
+    if (E <= 64) route_token<1>(logits, l_dtype, row, E, top_k, renorm, lane, id, weight);
+    else if (E <= 128) route_token<2>(logits, l_dtype, row, E, top_k, renorm, lane, id, weight);
+    else if (E <= 256) route_token<4>(logits, l_dtype, row, E, top_k, renorm, lane, id, weight);
+    else route_token<16>(logits, l_dtype, row, E, top_k, renorm, lane, id, weight);
 }
 
-// ---- the expert of a workgroup and its (token, choice) pairs ----------------------
-
-// The pairs [0, P) of the idx-th taken expert, in order, in `list`; returns
-// their number (0: fewer experts are taken) and the expert.  Called by the
-// whole workgroup.  `flags` holds kMoeMaxExperts / 32 words and two more.
-__device__ int expert_pairs(const int *__restrict__ ids, int P, int E, int idx, int tid, int nthreads, uint32_t *flags,
-                            uint16_t *list, int &expert) {
-    const int words = (E + 31) / 32;
-    for (int i = tid; i < words; i += nthreads) flags[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < P; i += nthreads) {
-        const int e = ids[i];
-        if (e >= 0) atomicOr(&flags[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    if (tid < 64) {
-        int left = idx, e = -1;
-        for (int w = 0; w < words && e < 0; ++w) {
-            uint32_t f = flags[w];
-            const int n = __popc(f);
-            if (left >= n) {
-                left -= n;
-                continue;
-            }
-            for (; left > 0; --left) f &= f - 1;
-            e = 32 * w + __ffs(f) - 1;
+// Index of the n-th set bit over `words` words, -1 if there are fewer.
+__device__ __forceinline__ int nth_bit(const uint32_t *bits, int words, int n) {
+    for (int w = 0; w < words; ++w) {
+        uint32_t f = bits[w];
+        const int c = __popc(f);
+        if (n >= c) {
+            n -= c;
+            continue;
         }
-        int count = 0;
-        if (e >= 0) {
-            for (int b = 0; b < P; b += 64) {
-                const bool hit = b + tid < P && ids[b + tid] == e;
-                const uint64_t m = __ballot(hit);
-                if (hit) list[count + __popcll(m & ((1ull << tid) - 1))] = (uint16_t)(b + tid);
-                count += __popcll(m);
-            }
-        }
-        if (tid == 0) {
-            flags[kMoeMaxExperts / 32] = (uint32_t)count;
-            flags[kMoeMaxExperts / 32 + 1] = (uint32_t)e;
+        for (; n > 0; --n) f &= f - 1;
+        return 32 * w + __ffs(f) - 1;
+    }
+    return -1;
+}
+
+// 16-bit words of a pair's hidden values.
+__host__ __device__ constexpr int64_t hid_words(int64_t F) { return (F + 511) / 512 * 1024; }
+
+// What the kernels hand on in the workspace.
+struct Plan {
+    int *ids;            // [P] expert of a (token, choice) pair, -1: none
+    float *weights;      // [P]
+    int *experts;        // [slots] the taken experts
+    int *start;          // [slots + 1] where an expert's pairs start, start[i] = start[i + 1]: not taken
+    int *pairs;          // [P] pairs by expert
+    uint16_t *hid;       // [P, steps of F, 2, 512] bf16: weight * hidden value, hi and lo terms
+    float *part;         // [P, H]
+};
+
+// More tokens: routing and the lists, by one workgroup of 16 waves.
+__global__ __launch_bounds__(1024) void moe_plan_kernel(const void *__restrict__ logits, int l_dtype, int T, int E,
+                                                        int top_k, int renorm, int slots, Plan plan) {
+    __shared__ int ids[kMoeChunk * kMoeMaxTopK];
+    __shared__ int count[kMoeMaxExperts], place[kMoeMaxExperts];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int P = T * top_k;
+    for (int e = tid; e < E; e += 1024) count[e] = 0;
+    for (int t = wave; t < T; t += 16) {
+        int id;
+        float w;
+        route_any(logits, l_dtype, t, E, top_k, renorm != 0, lane, id, w);
+        if (lane < top_k) {
+            ids[t * top_k + lane] = id;
+            plan.ids[t * top_k + lane] = id;
+            plan.weights[t * top_k + lane] = w;
         }
     }
     __syncthreads();
-    expert = (int)flags[kMoeMaxExperts / 32 + 1];
-    return (int)flags[kMoeMaxExperts / 32];
-}
-
-// ---- the product --------------------------------------------------------------
-
-// AT: activations fp16 (0), bf16 (1) or fp32 (2: hi and lo bf16 terms).
-constexpr int slots_rows(int at) { return at == 2 ? 2 : 4; }
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    const bf162_t v = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-// hi or lo bf16 terms of 8 fp32 values.
-__device__ __forceinline__ uint4 fp32_term(const uint4 &a, const uint4 &b, bool lo) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t o[4];
+    for (int i = tid; i < P; i += 1024)
+        if (ids[i] >= 0) atomicAdd(&count[ids[i]], 1);
+    __syncthreads();
+    if (wave == 0) {   // running sums over the experts: slots and starts
+        int slot = 0, start = 0;
+        for (int b = 0; b < E; b += 64) {
+            const int e = b + lane, n = e < E ? count[e] : 0;
+            int sum = n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x = __builtin_bit_cast(float, w[2 * i]), y = __builtin_bit_cast(float, w[2 * i + 1]);
-        const uint32_t hi = bf16_pair(x, y);
-        const float xh = __builtin_bit_cast(float, hi << 16), yh = __builtin_bit_cast(float, hi & 0xFFFF0000u);
-        // an infinite hi (infinity itself, or a value that rounds to it) has no rest
-        const uint32_t rest = bf16_pair(__builtin_isinf(xh) ? 0.f : x - xh, __builtin_isinf(yh) ? 0.f : y - yh);
-        o[i] = lo ? rest : hi;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(sum, d);
+                if (lane >= d) sum += o;
+            }
+            const uint64_t taken = __ballot(n > 0);
+            if (n > 0) {
+                const int s = slot + __popcll(taken & ((1ull << lane) - 1));
+                plan.experts[s] = e;
+                plan.start[s] = start + sum - n;
+                place[e] = start + sum - n;
+            }
+            slot += __popcll(taken);
+            start += __shfl(sum, 63);
+        }
+        for (int s = slot + lane; s <= slots; s += 64) plan.start[s] = start;
     }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    __syncthreads();
+    // Where a pair stands within its expert's changes the slot it is worked in, not its sums.
+    for (int i = tid; i < P; i += 1024)
+        if (ids[i] >= 0) plan.pairs[atomicAdd(&place[ids[i]], 1)] = i;
 }
+
+// ---- the products' parts --------------------------------------------------------
 
 template <int AT>
 __device__ __forceinline__ float4v_t mfma16(const uint4 &a, const uint4 &b, const float4v_t &c) {
@@ -195,286 +258,636 @@ __device__ __forceinline__ float4v_t mfma16(const uint4 &a, const uint4 &b, cons
                                                        0, 0, 0);
 }
 
-// The wave's share (steps wave, wave + nw, ...) of Q quads times SETS tiles of
-// activation rows.  row[q] / srow[q]: this lane's weight row and its scales;
-// arow[t]: this lane's activation row.  acc[t][q][v]: slot v, used where p = c.
-template <int AT, int SETS, int Q>
-__device__ __forceinline__ void product(const uint8_t *const (&row)[Q], const uint16_t *const (&srow)[Q],
-                                        const char *const (&arow)[SETS], int groups, int wave, int nw, int lane,
-                                        float4v_t (&acc)[SETS][Q]) {
-    constexpr int AQ = AT == 2 ? 8 : 4;   // 16-byte loads of a lane's 32 activations
-    const int p = lane >> 4, col = lane & 15, c = col & 3, ca = col >> 2;
-    const int steps = (groups + 3) / 4;
-    const bool lo = AT == 2 && (col & 3) >= 2;
-    for (int s = wave; s < steps; s += nw) {
-        const int wb = min(4 * s + c, groups - 1);
-        const int ab = min(4 * s + ca, groups - 1);
-        const bool wok = 4 * s + c < groups;
-        const uint32_t keep = 4 * s + ca < groups ? ~0u : 0u;
-        uint2 code[Q];
-        uint16_t sc[Q];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            code[q] = *reinterpret_cast<const uint2 *>(row[q] + (int64_t)wb * 32 + p * 8);
-            sc[q] = srow[q][wb];
+// AT: activations fp16 (0), bf16 (1) or fp32 (2: hi and lo terms in slots s and s + 2).
+constexpr int rows_per_set(int at) { return at == 2 ? 2 : 4; }
+
+// Rows of weights and scales: quads [0, Q / 2) in a, the others in b.
+struct Rows {
+    __amdgpu_buffer_rsrc_t a, b, sa, sb;
+};
+
+__device__ __forceinline__ Rows rows_of(const uint8_t *W, const uint16_t *S, int64_t na, int64_t nb, int ra, int rb,
+                                        int groups) {
+    ra = uniform(max(ra, 0)), rb = uniform(max(rb, 0));   // a clamp is a vector instruction
+    return {buffer_of(W + na * groups * 32, ra * groups * 32), buffer_of(W + nb * groups * 32, rb * groups * 32),
+            buffer_of(S + na * groups, ra * groups * 2), buffer_of(S + nb * groups, rb * groups * 2)};
+}
+
+// What a wave holds of one step's weights.  Loads with nothing to read (past the
+// end of a row, rows that are not there) have offsets out of range and return
+// zeros.
+template <int Q>
+struct Step {
+    uint2 code[Q];
+    uint32_t scale[Q];
+};
+
+// Offsets of step s in the weight rows, and in their scales.
+struct At {
+    int code, scale;
+};
+__device__ __forceinline__ At place_of(int s, int groups, int lane, bool live) {
+    const int p = lane >> 4, col = lane & 15, r = col >> 2, blk = 4 * s + (col & 3), at = r * groups + blk;
+    if (!live || blk >= groups) return {OUT_OF_RANGE, OUT_OF_RANGE};
+    return {at * 32 + p * 8, at * 2};
+}
+
+template <int Q>
+__device__ __forceinline__ void load_quad(Step<Q> &st, const Rows &w, const At &at, int groups, int q) {
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    st.scale[q] = __builtin_amdgcn_raw_buffer_load_b16(q < Q / 2 ? w.sa : w.sb, at.scale, 4 * (q % (Q / 2)) * groups * 2, 0);
+    const u32x2 v = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_raw_buffer_load_b64(q < Q / 2 ? w.a : w.b, at.code, 4 * (q % (Q / 2)) * groups * 32, 2));
+    st.code[q] = make_uint2(v[0], v[1]);
+}
+
+// Activations of the tiles' rows into LDS: operand i of set t of step s at ((s SETS + t) 4 + i) KB,
+// 16 bytes a lane, pair-interleaved.  Row j is read from x + off[j] bytes, none if negative.  A
+// thread takes 16 values of a row at a time.
+template <int SETS>
+__device__ __forceinline__ void stage(char *ops, const char *x, const int64_t *off, int groups, int tid, int nthreads) {
+    const int per_row = (groups + 3) / 4 * 32;
+    for (int i = tid; i < SETS * 4 * per_row; i += nthreads) {
+        const int j = i / per_row, k = i - j * per_row;   // row, sixteen of the row
+        const int s = k >> 5, ca = (k >> 3) & 3, p = (k >> 1) & 3, g = k & 1;
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+        if (off[j] >= 0 && k < groups * 8) {
+            const uint4 *v = reinterpret_cast<const uint4 *>(x + off[j] + k * 32);
+            v0 = v[0], v1 = v[1];
         }
-        uint4 a[SETS][4];   // the 4 operands of a lane's 32 activations, pair-interleaved
+        uint32_t w[8];
+        interleave16(v0, v1, w);
+        char *at = ops + ((s * SETS + j / 4) * 4 + 2 * g) * 1024 + (16 * p + 4 * ca + j % 4) * 16;
+        *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(at + 1024) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Where the up kernel leaves hidden value f of a pair, in 16-bit words, the lo term 512 behind: a
+// step's operands in the order in which the down kernels take them, [operand][ca][p][8].
+__device__ __forceinline__ int hidden_at(int f) {
+    const int k = f & 511, ca = k >> 7, p = (k >> 5) & 3, x = k & 15, j = x & 7;
+    const int i = ((k >> 4) & 1) * 2 + (j >> 2);
+    return (f >> 9) * 1024 + ((i * 4 + ca) * 4 + p) * 8 + (j & 3) * 2 + (x >> 3);
+}
+
+// Hidden values of pairs rowpair[j] into LDS (-1: none): row j is slots j % 2 and j % 2 + 2 of set j / 2.
+template <int SETS>
+__device__ __forceinline__ void stage_hidden(char *ops, const uint16_t *hid, const int *rowpair, int groups, int tid,
+                                             int nthreads) {
+    const int steps = (groups + 3) / 4, per_row = steps * 128;   // chunks of 16 bytes
+    for (int i = tid; i < SETS * 2 * per_row; i += nthreads) {
+        const int j = i / per_row, k = i - j * per_row;
+        const int s = k >> 7, term = (k >> 6) & 1, op = (k >> 4) & 3, ca = (k >> 2) & 3, p = k & 3;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (rowpair[j] >= 0 && 4 * s + ca < groups)
+            v = *reinterpret_cast<const uint4 *>(hid + ((int64_t)rowpair[j] * per_row + k) * 8);
+        *reinterpret_cast<uint4 *>(ops + ((s * SETS + j / 2) * 4 + op) * 1024 + (16 * p + 4 * ca + j % 2 + 2 * term) * 16) = v;
+    }
+}
+
+// The same with token j in row j of one set, no token in rows >= T.
+__device__ __forceinline__ void stage_tokens(char *ops, const char *x, int T, int groups, int tid, int nthreads) {
+    const int per_row = (groups + 3) / 4 * 32;
+    for (int i = tid; i < 4 * per_row; i += nthreads) {
+        const int j = i / per_row, k = i - j * per_row;
+        const int s = k >> 5, ca = (k >> 3) & 3, p = (k >> 1) & 3, g = k & 1;
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+        if (j < T && k < groups * 8) {
+            const uint4 *v = reinterpret_cast<const uint4 *>(x + (int64_t)j * groups * 256 + k * 32);
+            v0 = v[0], v1 = v[1];
+        }
+        uint32_t w[8];
+        interleave16(v0, v1, w);
+        char *at = ops + (s * 4 + 2 * g) * 1024 + (16 * p + 4 * ca + j) * 16;
+        *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(at + 1024) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// acc[t] += scale * (codes . a[t]) for one quad.
+template <int AT, int SETS>
+__device__ __forceinline__ void quad(uint2 code, uint32_t scale_bits, const uint4 (&a)[SETS][4], float4v_t (&acc)[SETS]) {
+    const uint64_t v = sign_nz_fields64<true>((uint64_t)code.x | ((uint64_t)code.y << 32));
+    uint32_t l[8], h[8];
+    weight_pairs2<0, true>(v, l[0], h[0]);
+    weight_pairs2<1, true>(v, l[1], h[1]);
+    weight_pairs2<2, true>(v, l[2], h[2]);
+    weight_pairs2<3, true>(v, l[3], h[3]);
+    weight_pairs2<4, true>(v, l[4], h[4]);
+    weight_pairs2<5, true>(v, l[5], h[5]);
+    weight_pairs2<6, true>(v, l[6], h[6]);
+    weight_pairs2<7, true>(v, l[7], h[7]);
+    const uint4 b[4] = {make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]),
+                        make_uint4(h[0], h[1], h[2], h[3]), make_uint4(h[4], h[5], h[6], h[7])};
+    const float scale = f16_bits_to_float((uint16_t)scale_bits);
+#pragma unroll
+    for (int t = 0; t < SETS; ++t) {
+        float4v_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d = mfma16<AT>(a[t][i], b[i], d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(scale, d[i], acc[t][i]);
+    }
+}
+
+// The sums of a wave into sums[q][t][slot][r][c].  Every lane stores, a lane without a used
+// sum into the spare words behind, at the same constant offsets from a base of its own: one
+// address register, and no matrix instruction is moved under a partial EXEC mask.
+template <int SETS, int Q>
+__device__ __forceinline__ void store_sums(float *sums, int lane, const float4v_t (&acc)[Q][SETS]) {
+    const int p = lane >> 4, col = lane & 15, r = col >> 2, c = col & 3;
+    int at = p == c ? r * 4 + c : Q * SETS * 64 + col;
+    asm volatile("" : "+v"(at));   // or the select is repeated for every store
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int t = 0; t < SETS; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sums[at + (q * SETS + t) * 64 + v * 16] = acc[q][t][v];
+}
+
+// One output of a wave's sums.
+template <int SETS>
+__device__ __forceinline__ float sum_of(const float *sums, int t, int q, int slot, int r) {
+    const float4 v = *reinterpret_cast<const float4 *>(sums + (q * SETS + t) * 64 + slot * 16 + r * 4);
+    return 0.5f * ((v.x + v.y) + (v.z + v.w));   // the weights were +-2
+}
+
+// Floats of a wave's sums.
+template <int SETS, int Q>
+__host__ __device__ constexpr int sums_floats() { return 2 * SETS * Q * 64; }
+
+// LDS of a workgroup: operands, the waves' sums, then what the kernel adds.
+template <int SETS>
+__host__ __device__ constexpr int ops_bytes(int groups) { return (groups + 3) / 4 * SETS * 4096; }
+
+// The compiler keeps the wave's LDS accesses on their sides.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int SETS, int Q>
+__device__ __forceinline__ void clear(float4v_t (&acc)[Q][SETS]) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int t = 0; t < SETS; ++t) acc[q][t] = (float4v_t){0.f, 0.f, 0.f, 0.f};
+}
+
+// The wave's units u0, u0 + stride, ... < units of Q quads each, over all of K.  G steps' loads are
+// in flight: each is refilled for the next G, or the next unit's first, as soon as it is used.
+// ready() fills the operands, rows(u) gives a unit's rows, done(u, sums) is called by the wave.
+template <int AT, int SETS, int Q, int G, typename Ready, typename RowsOf, typename Done>
+__device__ __forceinline__ void product(Ready ready, const char *ops, float *sums, int u0, int stride, int units,
+                                        int groups, int lane, RowsOf rows, Done done) {
+    const int steps = (groups + 3) / 4;
+    Step<Q> st[G];
+    {
+        const Rows w = rows(u0);
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const At at = place_of(j, groups, lane, u0 < units);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) load_quad<Q>(st[j], w, at, groups, q);
+        }
+    }
+    ready();   // the first weights are on their way
+    for (int u = u0; u < units; u += stride) {
+        float4v_t acc[Q][SETS];
+        clear<SETS, Q>(acc);
+        for (int s = 0;;) {
+            const bool turn = s + G >= steps;   // the next loads are the next unit's
+            const Rows w = rows(turn ? u + stride : u);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                uint4 a[SETS][4];
+                const char *op = ops + min(s + j, steps - 1) * (SETS * 4096) + lane * 16;
+#pragma unroll
+                for (int t = 0; t < SETS; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[t][i] = *reinterpret_cast<const uint4 *>(op + (t * 4 + i) * 1024);
+                const At at = place_of(turn ? j : s + G + j, groups, lane, !turn || u + stride < units);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    quad<AT, SETS>(st[j].code[q], st[j].scale[q], a, acc[q]);
+                    load_quad<Q>(st[j], w, at, groups, q);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if ((s += G) >= steps) break;
+        }
+        // the wave's own LDS accesses are served in order: only the compiler has to keep it
+        store_sums<SETS, Q>(sums, lane, acc);
+        wave_order();
+        done(u, sums);
+        wave_order();
+    }
+}
+
+// ---- kernels --------------------------------------------------------------------
+
+// Waves of a workgroup of the two products.  At most 128 registers, so that a CU holds two of
+// them (32 tokens, 64 experts of 2048 x 1024, 8 a token: up 36.5 -> 33.2 us, down 31.8 -> 29.2).
+constexpr int kWaves = 8;
+static_assert(kWaves > kMoeSmall, "waves that fetch while others route");
+
+// hid[pair][f] = silu(g) * u, 2 Q values f a unit: quads [0, Q / 2) are gate rows, the rest the up
+// rows of the same f.  SMALL: routes by itself while other waves fetch the tokens, the slots are the
+// tokens, and the first workgroup leaves ids and weights behind for the down kernel.
+template <int AT, int SETS, int Q, int G, bool SMALL>
+__global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__restrict__ X, const void *__restrict__ logits,
+                                                             int l_dtype, const uint8_t *__restrict__ GU,
+                                                             const uint16_t *__restrict__ GUS, Plan plan, int T, int E,
+                                                             int top_k, int renorm, int H, int F) {
+    static_assert(Q % 2 == 0, "gate and up quads");
+    constexpr int ROWS = SETS * rows_per_set(AT);
+    static_assert(!SMALL || ROWS >= kMoeSmall, "a slot a token");
+    extern __shared__ float4 lds4[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int groups = H >> 7;
+    char *ops = reinterpret_cast<char *>(lds4);
+    float *sums = reinterpret_cast<float *>(ops + ops_bytes<SETS>(groups));
+    int64_t *off = reinterpret_cast<int64_t *>(sums + kWaves * sums_floats<SETS, Q>());
+    int *rowpair = reinterpret_cast<int *>(off + ROWS);   // the pair of a row of the tiles, -1: none
+    float *rowweight = reinterpret_cast<float *>(rowpair + ROWS);
+    int *ids = rowpair + 2 * ROWS, *chosen = ids + kMoeSmall * kMoeMaxTopK;   // SMALL
+    uint32_t *bits = reinterpret_cast<uint32_t *>(chosen + 1);
+    float *weights = reinterpret_cast<float *>(bits + kMoeMaxExperts / 32);
+    int e, count = ROWS, start = 0;
+    if constexpr (SMALL) {
+        const int P = T * top_k, words = (E + 31) / 32;
+        if (wave < T) {   // T <= 4
+            int id;
+            float w;
+            route_any(logits, l_dtype, wave, E, top_k, renorm != 0, lane, id, w);
+            if (lane < top_k) {
+                ids[wave * top_k + lane] = id;
+                weights[wave * top_k + lane] = w;
+                if (blockIdx.x == 0 && blockIdx.y == 0) plan.ids[wave * top_k + lane] = id;
+            }
+        } else {
+            if (wave == kWaves - 1 && lane < words) bits[lane] = 0;
+            if constexpr (SMALL) stage_tokens(ops, X, T, groups, tid - 64 * T, 64 * (kWaves - T));
+        }
+        __syncthreads();
+        if (wave == 0) {
+            for (int i = lane; i < P; i += 64)
+                if (ids[i] >= 0) atomicOr(&bits[ids[i] >> 5], 1u << (ids[i] & 31));
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+            const int x = nth_bit(bits, words, blockIdx.y);
+            if (lane == 0) *chosen = x;
+            for (int t = 0; t < T; ++t) {
+                const uint64_t m = __ballot(lane < top_k && ids[t * top_k + min(lane, top_k - 1)] == x);
+                const int pr = m != 0 ? t * top_k + __ffsll((unsigned long long)m) - 1 : -1;
+                if (lane == 0) rowpair[t] = pr, rowweight[t] = weights[max(pr, 0)];
+            }
+            if (lane >= T && lane < ROWS) rowpair[lane] = -1;
+        }
+        __syncthreads();
+        e = __builtin_amdgcn_readfirstlane(*chosen);
+        if (e < 0) return;
+    } else {
+        start = uniform(plan.start[blockIdx.y]);
+        count = uniform(plan.start[blockIdx.y + 1]) - start;
+        if (count <= 0) return;
+        e = uniform(plan.experts[blockIdx.y]);
+    }
+    const int units = (F + 2 * Q - 1) / (2 * Q);
+    for (int base = 0; base < count; base += ROWS) {
+        product<AT, SETS, Q, G>(
+            [&]() __attribute__((always_inline)) {
+                if constexpr (!SMALL) {
+                    if (base > 0) __syncthreads();   // the operands of the chunk before are read
+                    if (tid < ROWS) {
+                        const int pr = base + tid < count ? plan.pairs[start + base + tid] : -1;
+                        off[tid] = pr >= 0 ? (int64_t)(pr / top_k) * H * 2 : -1;
+                        rowpair[tid] = pr;
+                        rowweight[tid] = pr >= 0 ? plan.weights[pr] : 0.f;
+                    }
+                    __syncthreads();
+                    stage<SETS>(ops, X, off, groups, tid, 64 * kWaves);
+                    __syncthreads();
+                }
+            },
+            ops, sums + wave * sums_floats<SETS, Q>(), blockIdx.x * kWaves + wave, gridDim.x * kWaves, units, groups, lane,
+            [&](int u) __attribute__((always_inline)) {
+                const int f0 = u * 2 * Q;
+                const int64_t g0 = (int64_t)e * 2 * F + f0;
+                return rows_of(GU, GUS, g0, g0 + F, min(2 * Q, F - f0), min(2 * Q, F - f0), groups);
+            },
+            [&](int u, const float *sm) __attribute__((always_inline)) {
+#pragma unroll
+                for (int o0 = 0; o0 < ROWS * 2 * Q; o0 += 64) {
+                    const int o = o0 + lane, ff = o % (2 * Q), i = min(o / (2 * Q), ROWS - 1), f = u * 2 * Q + ff;
+                    const float g = sum_of<SETS>(sm, i / 4, ff / 4, i % 4, ff % 4);
+                    const float y = sum_of<SETS>(sm, i / 4, ff / 4 + Q / 2, i % 4, ff % 4);
+                    const int pr = rowpair[i];
+                    const float h = g / (1.f + expf(-g)) * y * rowweight[i];
+                    const __bf16 hi = (__bf16)h, lo = (__bf16)(__builtin_isinf((float)hi) ? 0.f : h - (float)hi);   // infinity has no rest
+                    if (o < ROWS * 2 * Q && pr >= 0 && f < F) {
+                        uint16_t *at = plan.hid + (int64_t)pr * hid_words(F) + hidden_at(f);
+                        at[0] = __builtin_bit_cast(uint16_t, hi);
+                        at[512] = __builtin_bit_cast(uint16_t, lo);
+                    }
+                }
+            });
+    }
+}
+
+// part[pair][n] = (Wd h)[n], 4 Q values n a unit.
+template <int SETS, int Q, int G>
+__global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t *__restrict__ D,
+                                                               const uint16_t *__restrict__ DS, Plan plan, int H, int F) {
+    constexpr int ROWS = SETS * rows_per_set(2);
+    extern __shared__ float4 lds4[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int groups = F >> 7;
+    char *ops = reinterpret_cast<char *>(lds4);
+    float *sums = reinterpret_cast<float *>(ops + ops_bytes<SETS>(groups));
+    int *rowpair = reinterpret_cast<int *>(sums + kWaves * sums_floats<SETS, Q>());
+    const int start = uniform(plan.start[blockIdx.y]), count = uniform(plan.start[blockIdx.y + 1]) - start;
+    if (count <= 0) return;
+    const int e = uniform(plan.experts[blockIdx.y]);
+    const int units = (H + 4 * Q - 1) / (4 * Q);
+    for (int base = 0; base < count; base += ROWS) {
+        product<2, SETS, Q, G>(
+            [&]() __attribute__((always_inline)) {
+                if (base > 0) __syncthreads();   // the operands of the chunk before are read
+                if (tid < ROWS) rowpair[tid] = base + tid < count ? plan.pairs[start + base + tid] : -1;
+                __syncthreads();
+                stage_hidden<SETS>(ops, plan.hid, rowpair, groups, tid, 64 * kWaves);
+                __syncthreads();
+            },
+            ops, sums + wave * sums_floats<SETS, Q>(), blockIdx.x * kWaves + wave, gridDim.x * kWaves, units, groups, lane,
+            [&](int u) __attribute__((always_inline)) {
+                const int n0 = u * 4 * Q;
+                const int64_t r0 = (int64_t)e * H + n0;
+                return rows_of(D, DS, r0, r0 + 2 * Q, min(2 * Q, H - n0), min(2 * Q, H - n0 - 2 * Q), groups);
+            },
+            [&](int u, const float *sm) __attribute__((always_inline)) {
+#pragma unroll
+                for (int o0 = 0; o0 < ROWS * 4 * Q; o0 += 64) {
+                    const int o = o0 + lane, nn = o % (4 * Q), i = min(o / (4 * Q), ROWS - 1), n = u * 4 * Q + nn;
+                    const float y = sum_of<SETS>(sm, i / 2, nn / 4, i % 2, nn % 4) +
+                                    sum_of<SETS>(sm, i / 2, nn / 4, i % 2 + 2, nn % 4);
+                    const int pr = rowpair[i];
+                    if (o < ROWS * 4 * Q && pr >= 0 && n < H) plan.part[(int64_t)pr * H + n] = y;
+                }
+            });
+    }
+}
+
+// y[t][n] = the sum of the token's parts, in the order of its choices, 4 values a thread.
+__global__ __launch_bounds__(256) void moe_sum_kernel(Plan plan, void *__restrict__ Y, int y_dtype, int top_k, int H) {
+    const int t = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (n >= H) return;
+    const float *part = plan.part + (int64_t)t * top_k * H + n;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < top_k; j += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4 *>(part + (int64_t)min(j + i, top_k - 1) * H);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // a choice that there is not has nothing in its part
+            if (j + i >= top_k || plan.ids[t * top_k + j + i] < 0) continue;
+            y.x += v[i].x, y.y += v[i].y, y.z += v[i].z, y.w += v[i].w;
+        }
+    }
+    const int64_t at = (int64_t)t * H + n;
+    const float o[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (y_dtype == 2) store_out<2>(Y, at + i, o[i]);
+        else if (y_dtype == 1) store_out<1>(Y, at + i, o[i]);
+        else store_out<0>(Y, at + i, o[i]);
+    }
+}
+
+// Few tokens: a workgroup goes through every taken expert for its rows of Y.  Its waves take the
+// (expert, step) units in turn; the slots of the tiles are the tokens, and one that did not take
+// the expert at hand has zeros there.
+template <int SETS, int Q>
+__global__ __launch_bounds__(768) void moe_down_small_kernel(const uint8_t *__restrict__ D,
+                                                            const uint16_t *__restrict__ DS, Plan plan,
+                                                            void *__restrict__ Y, int y_dtype, int T, int E, int top_k,
+                                                            int H, int F, int nw) {
+    static_assert(SETS * rows_per_set(2) <= kMoeSmall, "tokens");
+    extern __shared__ float4 lds4[];
+    float *red = reinterpret_cast<float *>(lds4);
+    int *ids = reinterpret_cast<int *>(red + nw * sums_floats<SETS, Q>());
+    uint32_t *bits = reinterpret_cast<uint32_t *>(ids + kMoeSmall * kMoeMaxTopK);
+    int *experts = reinterpret_cast<int *>(bits + kMoeMaxExperts / 32);   // [P], then their number
+    int *pair = experts + kMoeSmall * kMoeMaxTopK + 1;                    // [P][T]: token's pair of an expert, -1: none
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int P = T * top_k, words = (E + 31) / 32;
+    for (int i = tid; i < P; i += 64 * nw) ids[i] = plan.ids[i];
+    for (int i = tid; i < words; i += 64 * nw) bits[i] = 0;
+    for (int i = tid; i < P * T; i += 64 * nw) pair[i] = -1;
+    __syncthreads();
+    if (wave == 0) {
+        for (int i = lane; i < P; i += 64)
+            if (ids[i] >= 0) atomicOr(&bits[ids[i] >> 5], 1u << (ids[i] & 31));
+        wave_order();
+        int n = 0;   // the set bits, in order
+        for (int w0 = 0; w0 < words; w0 += 2) {
+            const uint32_t word = w0 + (lane >> 5) < words ? bits[w0 + (lane >> 5)] : 0u;
+            const bool set = (word >> (lane & 31)) & 1u;
+            const uint64_t m = __ballot(set);
+            if (set) experts[n + __popcll(m & ((1ull << lane) - 1))] = 32 * w0 + lane;
+            n += __popcll(m);
+        }
+        if (lane == 0) experts[kMoeSmall * kMoeMaxTopK] = n;
+        for (int i = lane; i < P; i += 64) {   // the expert's place: the set bits before its own
+            const int e = ids[i];
+            if (e < 0) continue;
+            int at = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
+            for (int w = 0; w < e >> 5; ++w) at += __popc(bits[w]);
+            pair[at * T + i / top_k] = i;
+        }
+    }
+    __syncthreads();
+    const int taken = uniform(experts[kMoeSmall * kMoeMaxTopK]);
+    const int groups = F >> 7, n0 = blockIdx.x * 4 * Q, steps = (groups + 3) / 4, units = taken * steps;
+    const int ca = (lane & 15) >> 2, slot = lane & 3, per_pair = (int)hid_words(F) * 2;
+    const __amdgpu_buffer_rsrc_t rx = buffer_of(plan.hid, P * per_pair);
+    const int lane_at = (slot >> 1) * 1024 + (ca * 4 + (lane >> 4)) * 16;   // in a step's 2 KB
+
+    uint4 a[SETS][4];
+    Step<Q> st;
+    Rows w;
+    At at;
+    // Unit u: its rows' place, and the loads of its activations.
+    auto fetch = [&](int u) __attribute__((always_inline)) {
+        const bool live = u < units;
+        const int i = live ? u / steps : 0, s = live ? u - i * steps : 0, e = uniform(experts[i]);
 #pragma unroll
         for (int t = 0; t < SETS; ++t) {
-            const uint4 *x = reinterpret_cast<const uint4 *>(arow[t] + ((int64_t)ab * 128 + p * 32) * (AT == 2 ? 4 : 2));
-            uint4 raw[AQ];
+            const int tok = 2 * t + (slot & 1), pr = live && tok < T ? pair[i * T + min(tok, T - 1)] : -1;
+            const int off = pr >= 0 && 4 * s + ca < groups ? pr * per_pair + s * 2048 + lane_at : OUT_OF_RANGE;
 #pragma unroll
-            for (int i = 0; i < AQ; ++i) {
-                raw[i] = x[i];
-                raw[i].x &= keep, raw[i].y &= keep, raw[i].z &= keep, raw[i].w &= keep;
-            }
-            uint4 e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (AT == 2) e[i] = fp32_term(raw[2 * i], raw[2 * i + 1], lo);
-                else e[i] = raw[i];
-            }
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t w[8];
-                interleave16(e[2 * g], e[2 * g + 1], w);
-                a[t][2 * g] = make_uint4(w[0], w[1], w[2], w[3]);
-                a[t][2 * g + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+            for (int k = 0; k < 4; ++k) a[t][k] = load16(rx, off, k * 256);
         }
+        const int64_t r0 = (int64_t)e * H + n0;
+        w = rows_of(D, DS, r0, r0 + 2 * Q, min(2 * Q, H - n0), min(2 * Q, H - n0 - 2 * Q), groups);
+        at = place_of(s, groups, lane, live);
+    };
+    float4v_t acc[Q][SETS];
+    clear<SETS, Q>(acc);
+    int u = wave;
+    if (u < units) {
+        fetch(u);
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const uint64_t v = sign_nz_fields64<true>((uint64_t)code[q].x | ((uint64_t)code[q].y << 32));
-            uint32_t l[8], h[8];
-            weight_pairs2<0, true>(v, l[0], h[0]);
-            weight_pairs2<1, true>(v, l[1], h[1]);
-            weight_pairs2<2, true>(v, l[2], h[2]);
-            weight_pairs2<3, true>(v, l[3], h[3]);
-            weight_pairs2<4, true>(v, l[4], h[4]);
-            weight_pairs2<5, true>(v, l[5], h[5]);
-            weight_pairs2<6, true>(v, l[6], h[6]);
-            weight_pairs2<7, true>(v, l[7], h[7]);
-            const uint4 b[4] = {make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]),
-                                make_uint4(h[0], h[1], h[2], h[3]), make_uint4(h[4], h[5], h[6], h[7])};
-            const float scale = wok ? f16_bits_to_float(sc[q]) : 0.f;
+        for (int q = 0; q < Q; ++q) load_quad<Q>(st, w, at, groups, q);
+        for (;;) {
+            uint4 now[SETS][4];
 #pragma unroll
-            for (int t = 0; t < SETS; ++t) {
-                float4v_t d = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < SETS; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d = mfma16<AT>(a[t][i], b[i], d);
+                for (int k = 0; k < 4; ++k) now[t][k] = a[t][k];
+            fetch(u + nw);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][q][i] = fmaf(scale, d[i], acc[t][q][i]);
+            for (int q = 0; q < Q; ++q) {
+                quad<2, SETS>(st.code[q], st.scale[q], now, acc[q]);
+                load_quad<Q>(st, w, at, groups, q);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            u += nw;
+            if (u >= units) break;
         }
     }
-}
-
-// The wave's sums into red[wave][t][q][slot][r][c] (unused lanes into a spare word).
-template <int SETS, int Q>
-__device__ __forceinline__ void store_sums(float *red, int wave, int nw, int lane, const float4v_t (&acc)[SETS][Q]) {
-    const int p = lane >> 4, col = lane & 15, r = col >> 2, c = col & 3;
-    const int spare = nw * SETS * Q * 64 + lane;
-#pragma unroll
-    for (int t = 0; t < SETS; ++t)
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int at = ((wave * SETS + t) * Q + q) * 64 + v * 16 + r * 4 + c;
-                red[p == c ? at : spare] = acc[t][q][v];
-            }
-}
-
-template <int SETS, int Q>
-__device__ __forceinline__ float sum_of(const float *red, int nw, int t, int q, int slot, int r) {
-    float y = 0.f;
-    for (int w = 0; w < nw; ++w) {
-        const float4 v = *reinterpret_cast<const float4 *>(red + ((w * SETS + t) * Q + q) * 64 + slot * 16 + r * 4);
-        y += (v.x + v.y) + (v.z + v.w);
-    }
-    return 0.5f * y;   // the weights were +-2
-}
-
-// LDS: sums, then the expert flags, then the pair list.
-template <int SETS, int Q>
-constexpr size_t red_words(int nw) {
-    return (size_t)nw * SETS * Q * 64 + 64;
-}
-constexpr int FLAG_WORDS = kMoeMaxExperts / 32 + 2;
-
-// h[pair][f] = silu(g) * u.  Quads [0, Q/2) are gate rows, the rest the up rows of the same f.
-template <int AT, int SETS, int Q>
-__global__ __launch_bounds__(64 * E_MAX_WAVES) void moe_up_kernel(const char *__restrict__ X,
-                                                                const uint8_t *__restrict__ GU,
-                                                                const uint16_t *__restrict__ GUS,
-                                                                const int *__restrict__ ids, float *__restrict__ Hid,
-                                                                int P, int E, int top_k, int H, int F, int nw) {
-    static_assert(Q % 2 == 0, "gate and up quads");
-    extern __shared__ float4 lds4[];
-    float *red = reinterpret_cast<float *>(lds4);
-    uint32_t *flags = reinterpret_cast<uint32_t *>(red + red_words<SETS, Q>(nw));
-    uint16_t *list = reinterpret_cast<uint16_t *>(flags + FLAG_WORDS);
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int e;
-    const int count = expert_pairs(ids, P, E, blockIdx.y, tid, 64 * nw, flags, list, e);
-    if (count == 0) return;
-    const int groups = H >> 7;
-    const int f0 = blockIdx.x * 2 * Q;
-    const int col = lane & 15, r = col >> 2, slot = col & 3;
-    const uint8_t *row[Q];
-    const uint16_t *srow[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int f = min(f0 + 4 * (q % (Q / 2)) + r, F - 1);
-        const int64_t n = (int64_t)e * 2 * F + (q < Q / 2 ? 0 : F) + f;
-        row[q] = GU + n * (H / 4);
-        srow[q] = GUS + n * groups;
-    }
-    constexpr int RPS = slots_rows(AT);
-    for (int base = 0; base < count; base += RPS * SETS) {
-        const char *arow[SETS];
-#pragma unroll
-        for (int t = 0; t < SETS; ++t)
-            arow[t] = X + (int64_t)(list[min(base + t * RPS + slot, count - 1)] / top_k) * H * 2;
-        float4v_t acc[SETS][Q];
-#pragma unroll
-        for (int t = 0; t < SETS; ++t)
-#pragma unroll
-            for (int q = 0; q < Q; ++q) acc[t][q] = (float4v_t){0.f, 0.f, 0.f, 0.f};
-        product<AT, SETS, Q>(row, srow, arow, groups, wave, nw, lane, acc);
-        if (base > 0) __syncthreads();   // the sums of the chunk before are read
-        store_sums<SETS, Q>(red, wave, nw, lane, acc);
-        __syncthreads();
-        for (int o = tid; o < SETS * RPS * 2 * Q; o += 64 * nw) {
-            const int ff = o % (2 * Q), i = o / (2 * Q);
-            if (base + i >= count || f0 + ff >= F) continue;
-            const float g = sum_of<SETS, Q>(red, nw, i / RPS, ff / 4, i % RPS, ff % 4);
-            const float u = sum_of<SETS, Q>(red, nw, i / RPS, ff / 4 + Q / 2, i % RPS, ff % 4);
-            Hid[(int64_t)list[base + i] * F + f0 + ff] = g / (1.f + expf(-g)) * u;
+    store_sums<SETS, Q>(red + wave * sums_floats<SETS, Q>(), lane, acc);
+    __syncthreads();
+    for (int o = tid >> 2; o < T * 4 * Q; o += 16 * nw) {   // the 4 lanes of a DPP quad share an output
+        const int nn = o % (4 * Q), i = o / (4 * Q);
+        float y = 0.f;
+        for (int w = tid & 3; w < nw; w += 4) {
+            const float *sm = red + w * sums_floats<SETS, Q>();
+            y += sum_of<SETS>(sm, i / 2, nn / 4, i % 2, nn % 4) + sum_of<SETS>(sm, i / 2, nn / 4, i % 2 + 2, nn % 4);
         }
+        y += __builtin_bit_cast(float, dpp<0xB1>(__builtin_bit_cast(uint32_t, y)));
+        y += __builtin_bit_cast(float, dpp<0x4E>(__builtin_bit_cast(uint32_t, y)));
+        if ((tid & 3) != 0 || n0 + nn >= H) continue;
+        const int64_t at = (int64_t)i * H + n0 + nn;
+        if (y_dtype == 2) store_out<2>(Y, at, y);
+        else if (y_dtype == 1) store_out<1>(Y, at, y);
+        else store_out<0>(Y, at, y);
     }
 }
 
-// part[pair][n] = weight * (Wd h)[n].
-template <int SETS, int Q>
-__global__ __launch_bounds__(64 * E_MAX_WAVES) void moe_down_kernel(const float *__restrict__ Hid,
-                                                                  const uint8_t *__restrict__ D,
-                                                                  const uint16_t *__restrict__ DS,
-                                                                  const int *__restrict__ ids,
-                                                                  const float *__restrict__ weights,
-                                                                  float *__restrict__ part, int P, int E, int H, int F,
-                                                                  int nw) {
-    extern __shared__ float4 lds4[];
-    float *red = reinterpret_cast<float *>(lds4);
-    uint32_t *flags = reinterpret_cast<uint32_t *>(red + red_words<SETS, Q>(nw));
-    uint16_t *list = reinterpret_cast<uint16_t *>(flags + FLAG_WORDS);
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int e;
-    const int count = expert_pairs(ids, P, E, blockIdx.y, tid, 64 * nw, flags, list, e);
-    if (count == 0) return;
-    const int groups = F >> 7;
-    const int n0 = blockIdx.x * 4 * Q;
-    const int col = lane & 15, r = col >> 2, slot = col & 3;
-    const uint8_t *row[Q];
-    const uint16_t *srow[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int64_t n = (int64_t)e * H + min(n0 + 4 * q + r, H - 1);
-        row[q] = D + n * (F / 4);
-        srow[q] = DS + n * groups;
-    }
-    constexpr int RPS = slots_rows(2);
-    for (int base = 0; base < count; base += RPS * SETS) {
-        const char *arow[SETS];
-#pragma unroll
-        for (int t = 0; t < SETS; ++t)
-            arow[t] = reinterpret_cast<const char *>(Hid + (int64_t)list[min(base + t * RPS + (slot & 1), count - 1)] * F);
-        float4v_t acc[SETS][Q];
-#pragma unroll
-        for (int t = 0; t < SETS; ++t)
-#pragma unroll
-            for (int q = 0; q < Q; ++q) acc[t][q] = (float4v_t){0.f, 0.f, 0.f, 0.f};
-        product<2, SETS, Q>(row, srow, arow, groups, wave, nw, lane, acc);
-        if (base > 0) __syncthreads();   // the sums of the chunk before are read
-        store_sums<SETS, Q>(red, wave, nw, lane, acc);
-        __syncthreads();
-        for (int o = tid; o < SETS * RPS * 4 * Q; o += 64 * nw) {
-            const int nn = o % (4 * Q), i = o / (4 * Q);
-            if (base + i >= count || n0 + nn >= H) continue;
-            const int t = i / RPS, k = i % RPS;
-            const float y = sum_of<SETS, Q>(red, nw, t, nn / 4, k, nn % 4) +
-                            sum_of<SETS, Q>(red, nw, t, nn / 4, k + 2, nn % 4);
-            const int pair = list[base + i];
-            part[(int64_t)pair * H + n0 + nn] = weights[pair] * y;
-        }
-    }
-}
-
-// y[t][n] = the sum of the token's parts, in the order of its choices.
-__global__ __launch_bounds__(256) void moe_sum_kernel(const float *__restrict__ part, const int *__restrict__ ids,
-                                                      void *__restrict__ Y, int y_dtype, int top_k, int H) {
-    const int t = blockIdx.y;
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= H) return;
-    float y = 0.f;
-    for (int j = 0; j < top_k; ++j)
-        if (ids[t * top_k + j] >= 0) y += part[((int64_t)t * top_k + j) * H + n];
-    const int64_t at = (int64_t)t * H + n;
-    if (y_dtype == 2) store_out<2>(Y, at, y);
-    else if (y_dtype == 1) store_out<1>(Y, at, y);
-    else store_out<0>(Y, at, y);
-}
-
-int waves_of(int64_t K) {
-    const int64_t steps = (K + E_STEP - 1) / E_STEP;
-    return (int)(steps < E_MAX_WAVES ? steps : E_MAX_WAVES);
-}
-
-template <int SETS, int Q>
-size_t lds_bytes(int nw, int64_t P) {
-    return (red_words<SETS, Q>(nw) + FLAG_WORDS) * 4 + (size_t)P * 2;
-}
+// ---- launches -------------------------------------------------------------------
 
 constexpr size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// One chunk of at most kMoeChunk tokens.
+Plan plan_of(void *ws, int64_t P, int64_t H, int64_t F) {
+    char *w = static_cast<char *>(ws);
+    auto take = [&](size_t n) {
+        char *at = w;
+        w += align256(n);
+        return at;
+    };
+    Plan p;
+    p.ids = reinterpret_cast<int *>(take((size_t)P * 4));
+    p.weights = reinterpret_cast<float *>(take((size_t)P * 4));
+    p.experts = reinterpret_cast<int *>(take((size_t)P * 4));
+    p.start = reinterpret_cast<int *>(take((size_t)(P + 1) * 4));
+    p.pairs = reinterpret_cast<int *>(take((size_t)P * 4));
+    p.hid = reinterpret_cast<uint16_t *>(take((size_t)P * hid_words(F) * 2));
+    p.part = reinterpret_cast<float *>(w);
+    return p;
+}
+
+// Workgroups for `slots` experts' `units`: about two a CU, each wave with as many units as the others.
+int workgroups(int64_t units, int slots) {
+    const int64_t most = std::max<int64_t>(1, 512 / slots), waves = std::min((units + kWaves - 1) / kWaves, most) * kWaves;
+    const int64_t each = (units + waves - 1) / waves;
+    return (int)(((units + each - 1) / each + kWaves - 1) / kWaves);
+}
+
+constexpr size_t kLds = 160 * 1024;
+
+template <int AT, int SETS, int Q, int G, bool SMALL>
+hipError_t launch_up(const MoeArgs &a, const Plan &plan, int slots) {
+    const size_t lds = ops_bytes<SETS>((int)(a.H / 128)) + kWaves * sums_floats<SETS, Q>() * 4 +
+                       SETS * rows_per_set(AT) * 16 + (SMALL ? kMoeSmall * kMoeMaxTopK * 8 + 4 + kMoeMaxExperts / 8 : 0);
+    if constexpr (SETS > 1)
+        if (lds > kLds) return launch_up<AT, SETS / 2, Q, G, SMALL>(a, plan, slots);
+    const dim3 g((unsigned)workgroups((a.F + 2 * Q - 1) / (2 * Q), slots), (unsigned)slots), b(64 * kWaves);
+    constexpr auto kern = &moe_up_kernel<AT, SETS, Q, G, SMALL>;
+    const hipError_t e = raise_lds_limit<kern>(lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, g, b, lds, a.stream, static_cast<const char *>(a.X), a.logits, a.l_dtype, a.GU, a.GUS, plan,
+                       (int)a.T, (int)a.E, (int)a.top_k, a.renormalize, (int)a.H, (int)a.F);
+    return hipGetLastError();
+}
+
+template <int SETS, int Q, int G>
+hipError_t launch_down(const MoeArgs &a, const Plan &plan, int slots) {
+    const size_t lds = ops_bytes<SETS>((int)(a.F / 128)) + kWaves * sums_floats<SETS, Q>() * 4 + SETS * rows_per_set(2) * 4;
+    if constexpr (SETS > 1)
+        if (lds > kLds) return launch_down<SETS / 2, Q, G>(a, plan, slots);
+    const dim3 g((unsigned)workgroups((a.H + 4 * Q - 1) / (4 * Q), slots), (unsigned)slots), b(64 * kWaves);
+    constexpr auto kern = &moe_down_kernel<SETS, Q, G>;
+    const hipError_t e = raise_lds_limit<kern>(lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, g, b, lds, a.stream, a.D, a.DS, plan, (int)a.H, (int)a.F);
+    return hipGetLastError();
+}
+
+template <int SETS, int Q>
+hipError_t launch_down_small(const MoeArgs &a, const Plan &plan) {
+    const int64_t units = a.T * a.top_k * ((a.F + 511) / 512);   // at most
+    const int nw = (int)(units < 12 ? units : 12);
+    const dim3 g((unsigned)((a.H + 4 * Q - 1) / (4 * Q))), b(64 * nw);
+    const size_t lds = (size_t)nw * sums_floats<SETS, Q>() * 4 + kMoeSmall * kMoeMaxTopK * 4 * (2 + kMoeSmall) +
+                       kMoeMaxExperts / 8 + 4;
+    constexpr auto kern = &moe_down_small_kernel<SETS, Q>;
+    const hipError_t e = raise_lds_limit<kern>(lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, g, b, lds, a.stream, a.D, a.DS, plan, a.Y, a.y_dtype, (int)a.T, (int)a.E, (int)a.top_k,
+                       (int)a.H, (int)a.F, nw);
+    return hipGetLastError();
+}
+
+// Steps of K that come in twos rather than in fours.
+bool few_steps(int64_t K) { return (K + 511) / 512 % 4 == 1 || (K + 511) / 512 % 4 == 2; }
+
+template <int SETS, bool SMALL>
+hipError_t up(const MoeArgs &a, const Plan &plan, int slots) {
+    if (few_steps(a.H))
+        return a.x_dtype == 0 ? launch_up<0, SETS, 4, 2, SMALL>(a, plan, slots) : launch_up<1, SETS, 4, 2, SMALL>(a, plan, slots);
+    return a.x_dtype == 0 ? launch_up<0, SETS, 2, 4, SMALL>(a, plan, slots) : launch_up<1, SETS, 2, 4, SMALL>(a, plan, slots);
+}
+
 hipError_t launch_chunk(const MoeArgs &a) {
     const int P = (int)(a.T * a.top_k);
-    char *w = static_cast<char *>(a.ws);
-    int *ids = reinterpret_cast<int *>(w);
-    w += align256((size_t)P * 4);
-    float *weights = reinterpret_cast<float *>(w);
-    w += align256((size_t)P * 4);
-    float *hid = reinterpret_cast<float *>(w);
-    w += align256((size_t)P * a.F * 4);
-    float *part = reinterpret_cast<float *>(w);
-    hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)a.T), dim3(64), 0, a.stream, a.logits, a.l_dtype, (int)a.E,
-                       (int)a.top_k, a.renormalize, ids, weights);
-    const unsigned slots = (unsigned)(a.E < P ? a.E : P);
-    {
-        constexpr int SETS = 1, Q = 4;
-        const int nw = waves_of(a.H);
-        const dim3 g((unsigned)((a.F + 2 * Q - 1) / (2 * Q)), slots), b(64 * nw);
-        const size_t lds = lds_bytes<SETS, Q>(nw, P);
-        if (a.x_dtype == 0)
-            hipLaunchKernelGGL((moe_up_kernel<0, SETS, Q>), g, b, lds, a.stream, static_cast<const char *>(a.X), a.GU,
-                               a.GUS, ids, hid, P, (int)a.E, (int)a.top_k, (int)a.H, (int)a.F, nw);
-        else
-            hipLaunchKernelGGL((moe_up_kernel<1, SETS, Q>), g, b, lds, a.stream, static_cast<const char *>(a.X), a.GU,
-                               a.GUS, ids, hid, P, (int)a.E, (int)a.top_k, (int)a.H, (int)a.F, nw);
+    const Plan plan = plan_of(a.ws, P, a.H, a.F);
+    const int slots = (int)(a.E < P ? a.E : P);
+    hipError_t e;
+    if (a.T <= kMoeSmall) {
+        e = up<1, true>(a, plan, slots);
+        if (e != hipSuccess) return e;
+        // More rows a workgroup once they fill the chip all the same (T = 4: H = 5120, 17.3 -> 15.2 us; H = 2048, 5 -> 7)
+        if (a.T <= 2) return launch_down_small<1, 2>(a, plan);
+        return a.H < 4096 ? launch_down_small<2, 2>(a, plan) : launch_down_small<2, 4>(a, plan);
     }
-    {
-        constexpr int SETS = 1, Q = 4;
-        const int nw = waves_of(a.F);
-        const dim3 g((unsigned)((a.H + 4 * Q - 1) / (4 * Q)), slots), b(64 * nw);
-        const size_t lds = lds_bytes<SETS, Q>(nw, P);
-        hipLaunchKernelGGL((moe_down_kernel<SETS, Q>), g, b, lds, a.stream, hid, a.D, a.DS, ids, weights, part, P,
-                           (int)a.E, (int)a.H, (int)a.F, nw);
-    }
-    hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, a.stream, part,
-                       ids, a.Y, a.y_dtype, (int)a.top_k, (int)a.H);
+    hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.logits, a.l_dtype, (int)a.T, (int)a.E,
+                       (int)a.top_k, a.renormalize, slots, plan);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // A second set of slots once the experts have more than two tokens in the mean.
+    e = P > 2 * slots ? up<2, false>(a, plan, slots) : up<1, false>(a, plan, slots);
+    if (e != hipSuccess) return e;
+    e = few_steps(a.F) ? launch_down<2, 4, 2>(a, plan, slots) : launch_down<2, 2, 4>(a, plan, slots);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256), 0, a.stream, plan,
+                       a.Y, a.y_dtype, (int)a.top_k, (int)a.H);
     return hipGetLastError();
 }
 
@@ -482,7 +895,8 @@ hipError_t launch_chunk(const MoeArgs &a) {
 
 size_t moe_workspace(int64_t T, int64_t top_k, int64_t H, int64_t F) {
     const int64_t P = (T < kMoeChunk ? T : kMoeChunk) * top_k;
-    return 2 * align256((size_t)P * 4) + align256((size_t)P * F * 4) + align256((size_t)P * H * 4);
+    return 4 * align256((size_t)P * 4) + align256((size_t)(P + 1) * 4) + align256((size_t)P * hid_words(F) * 2) +
+           align256((size_t)P * H * 4);
 }
 
 hipError_t launch_moe(const MoeArgs &a0) {

@@ -5,9 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "tern_device.h"
+#include "tern_launch.h"
 
 namespace tern {
 
@@ -47,24 +46,6 @@ __device__ __forceinline__ bf168_t decode8(uint32_t c, float s) {
     w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
     w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
     return __builtin_bit_cast(bf168_t, make_uint4(w[0], w[1], w[2], w[3]));
-}
-
-// Raise a kernel's dynamic-LDS limit once per device and kernel (a per-process
-// attribute; not a stream operation).
-template <auto Kern>
-inline hipError_t raise_lds_limit(size_t lds) {
-    if (lds <= 64 * 1024) return hipSuccess;
-    static std::atomic<uint64_t> done_mask{0};
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(done_mask.load(std::memory_order_acquire) & bit)) {
-        e = hipFuncSetAttribute(reinterpret_cast<const void *>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-        if (e != hipSuccess) return e;
-        done_mask.fetch_or(bit, std::memory_order_acq_rel);
-    }
-    return hipSuccess;
 }
 
 }  // namespace tern

@@ -77,6 +77,18 @@ def test_layer(T, E, k, H, F, xd, yd, ld, renorm):
     R.assert_close(y, want, bound, "moe")
 
 
+@pytest.mark.parametrize("T,H,F", [(1, 16384, 128), (3, 128, 16384), (7, 16384, 128), (5, 128, 16384),
+                                   (21, 7040, 128), (21, 128, 7168)])
+def test_widths_at_the_limit(T, H, F):
+    """Operands that fill LDS, and widths at which fewer tokens of an expert fit at a time."""
+    print(f"moe T={T} H={H} F={F}", flush=True)
+    L = Layer(2, H, F, T + H)
+    x, lg = inputs(T, 2, H, "bf16", T + F, "f32")
+    y = L.run(x, lg, 1, True, "f32")
+    want, bound = L.want(x, lg, 1, True, "f32")
+    R.assert_close(y, want, bound, "moe")
+
+
 @pytest.mark.parametrize("T,E,H,F", [(1, 3, 256, 128), (3, 3, 1152, 256), (6, 2, 128, 384), (20, 4, 512, 128),
                                      (70, 4, 128, 256)])
 @pytest.mark.parametrize("xd", ["f16", "bf16"])

@@ -67,6 +67,7 @@ def moe(X=P, xd=BF16, lg=P, ld=F32, gu=P, gus=P, dn=P, ds=P, Y=P, yd=BF16, T=2, 
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), SHAPE), (dict(E=-1), SHAPE), (dict(H=-128), SHAPE), (dict(F=-128), SHAPE), (dict(k=0), SHAPE),
     (dict(k=9), SHAPE), (dict(E=0, k=1), SHAPE), (dict(H=(1 << 30) + 128), SHAPE), (dict(T=1 << 31), SHAPE),
+    (dict(H=16384 + 128), SHAPE), (dict(F=16384 + 128), SHAPE),
     (dict(H=192), GROUP), (dict(F=64), GROUP), (dict(G=0), GROUP), (dict(G=-128), GROUP),
     (dict(G=64), UNSUP), (dict(E=1025), UNSUP), (dict(E=64, k=33), UNSUP),
     (dict(xd=F32), DTYPE), (dict(ld=4), DTYPE), (dict(yd=4), DTYPE),
