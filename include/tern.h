@@ -245,7 +245,8 @@ tern_status tern_mx_dequant(const uint8_t *codes, const uint8_t *exps, void *W, 
 /*
  * tern_mx_matmul -- Y[M,N] = X[M,K] . W^T, W[N,K] held as codes and exps,
  * X in TERN_F16 or TERN_BF16, sums in fp32, Y in any of the three types,
- * rounded once (nearest even).  Any M.  X 16-byte aligned, Y to its element.
+ * rounded once (nearest even).  Any M, K <= 2^24.  X 16-byte aligned, Y to its
+ * element.
  * The products are exact.  An infinity or NaN in a row of X reaches that row
  * of Y only, one in a row of W (a block with exponent 255, or values beyond
  * the fp32 range) that column only.
@@ -255,7 +256,7 @@ tern_status tern_mx_matmul(const void *X, tern_dtype x_dtype, const uint8_t *cod
 
 /*
  * tern_mx_matmul_mx -- the same product with X[M,K] held as x_codes and
- * x_exps too (for instance from tern_mx_quantize).
+ * x_exps too (for instance from tern_mx_quantize).  K <= 2^24.
  */
 tern_status tern_mx_matmul_mx(const uint8_t *x_codes, const uint8_t *x_exps, const uint8_t *codes,
                               const uint8_t *exps, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,

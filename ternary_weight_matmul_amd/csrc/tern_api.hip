@@ -12,6 +12,9 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxK = int64_t(1) << 30;
+// Products with microscaled weights: offsets inside the rows of one workgroup are 32-bit (72 rows
+// of K / 2 bytes).
+constexpr int64_t kMxMaxK = int64_t(1) << 24;
 constexpr int64_t kMaxProduct = int64_t(1) << 62;
 constexpr size_t kGemvLdsLimit = 152 * 1024;
 
@@ -166,7 +169,7 @@ tern_status check_mx_args(const void *codes, const void *exps, const void *dense
 // Both products: XE is null where X holds 16-bit values.
 tern_status check_mx_product(const void *X, const void *XE, bool mx, const void *W, const void *WE, const void *Y,
                              tern_dtype y_dtype, int64_t M, int64_t N, int64_t K) {
-    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return TERN_ERR_SHAPE;
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMxMaxK) return TERN_ERR_SHAPE;
     if (!product_ok(M, N) || !product_ok(M, K) || !product_ok(N, K)) return TERN_ERR_SHAPE;
     if (K % TERN_MX_BLOCK != 0) return TERN_ERR_GROUP;
     if (!known_dtype(y_dtype)) return TERN_ERR_DTYPE;

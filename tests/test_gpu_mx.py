@@ -153,6 +153,30 @@ def test_matmul_mx(M, N, K, yd):
     R.assert_close(y, want, R.product_bound(X, W, want, DT[yd]), "mx_matmul_mx")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "mx"])
+def test_largest_k(kind):
+    """Offsets of a row near 2^24 values, with sums that are exact: ones and halves, few of them."""
+    M, N, K = 2, 73, 1 << 24
+    print(f"K = 2^24 {kind}", flush=True)
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=DEV)
+    exps = torch.full((N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    at = torch.arange(0, K // 2, 4099, device=DEV)
+    codes[:, at] = 0x12          # 1 and 0.5
+    codes[:, -1] = 0x21
+    codes[72, -1] = 0
+    x = torch.ones((M, K), dtype=torch.bfloat16, device=DEV)
+    x[1] = 2
+    if kind == "mx":
+        y = tern.mx_matmul_mx(*tern.mx_quantize(x), codes, exps, torch.float32)
+    else:
+        y = tern.mx_matmul(x, codes, exps, torch.float32)
+    n = at.numel() + (0 if int(at[-1]) == K // 2 - 1 else 1)
+    want = torch.full((M, N), 1.5 * n)
+    want[:, 72] -= 1.5
+    want[1] *= 2
+    assert torch.equal(y.cpu(), want)
+
+
 @pytest.mark.parametrize("M,N,K", SHAPES)
 @pytest.mark.parametrize("kind", ["bf16", "f16", "mx"])
 def test_exact_arithmetic(M, N, K, kind):

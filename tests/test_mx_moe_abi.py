@@ -37,7 +37,7 @@ def mm(X=P, xd=BF16, W=P, S=P, Y=P, yd=BF16, M=2, N=16, K=64):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-32), SHAPE), (dict(N=1 << 31), SHAPE),
-    (dict(K=(1 << 30) + 32), SHAPE), (dict(K=40), GROUP), (dict(xd=F32), DTYPE), (dict(xd=9), DTYPE),
+    (dict(K=(1 << 30) + 32), SHAPE), (dict(K=(1 << 24) + 32), SHAPE), (dict(K=40), GROUP), (dict(xd=F32), DTYPE), (dict(xd=9), DTYPE),
     (dict(yd=5), DTYPE), (dict(X=0), NULL), (dict(W=0), NULL), (dict(S=0), NULL), (dict(Y=0), NULL),
     (dict(K=0, Y=0), NULL), (dict(X=P + 2), ALIGN), (dict(W=P + 8), ALIGN), (dict(Y=P + 1), ALIGN),
     (dict(Y=P + 2, yd=F32), ALIGN), (dict(M=0, X=0, W=0, S=0, Y=0), OK), (dict(N=0, X=0, W=0, S=0, Y=0), OK),
@@ -51,7 +51,8 @@ def mmx(X=P, XS=P, W=P, S=P, Y=P, yd=BF16, M=2, N=16, K=64):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(M=-1), SHAPE), (dict(K=40), GROUP), (dict(yd=5), DTYPE), (dict(X=0), NULL), (dict(XS=0), NULL),
+    (dict(M=-1), SHAPE), (dict(K=(1 << 24) + 32), SHAPE), (dict(K=40), GROUP), (dict(yd=5), DTYPE), (dict(X=0), NULL),
+    (dict(XS=0), NULL),
     (dict(W=0), NULL), (dict(S=0), NULL), (dict(Y=0), NULL), (dict(X=P + 8), ALIGN), (dict(W=P + 8), ALIGN),
     (dict(M=0, X=0, XS=0, W=0, S=0, Y=0), OK),
 ])
