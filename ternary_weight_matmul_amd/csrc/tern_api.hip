@@ -199,7 +199,7 @@ tern_status mx_product(const void *X, const uint8_t *XE, int x_dtype, const uint
     a.N = N;
     a.K = K;
     a.stream = stream;
-    return from_hip(M > 32 && tern::mx_gemm_fits(a) ? tern::launch_mx_gemm(a) : tern::launch_mx_gemv(a));
+    return from_hip(tern::mx_gemm_wins(a) ? tern::launch_mx_gemm(a) : tern::launch_mx_gemv(a));
 }
 
 bool moe_sizes_ok(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {

@@ -34,8 +34,8 @@ hipError_t launch_mx_dequant(const uint8_t *codes, const uint8_t *exps, void *W,
                              hipStream_t stream);
 // Product for few rows: waves split K, weights are read once per row chunk.
 hipError_t launch_mx_gemv(const MxArgs &a);
-// Product for many rows: LDS-staged tiles.
-bool mx_gemm_fits(const MxArgs &a);
+// Product for many rows: LDS-staged tiles, and where they are the faster choice.
+bool mx_gemm_wins(const MxArgs &a);
 hipError_t launch_mx_gemm(const MxArgs &a);
 
 }  // namespace tern

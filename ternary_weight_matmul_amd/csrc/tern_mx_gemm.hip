@@ -29,6 +29,7 @@
 // Bound: the matrix cores.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "tern_device.h"
@@ -413,21 +414,35 @@ hipError_t launch_t(const MxArgs &a) {
     return hipGetLastError();
 }
 
+// Big tiles (256 x 256, with 4-bit X 256 x 192) or small ones (64 x 128).  A step of a big tile takes
+// 2.4 times a small one's, 3.4 times when every CU has one (2.6 with 4-bit X, either way), and a CU
+// holds one big tile at a time; up to 256 small ones take as long as one.  Measured, K = 5120, us:
+//   16-bit X: 512 -> 5120: big 120, small 59; 256 -> 17408: 124, 104; 1024 -> 5120: 122, 95;
+//   512 -> 17408: 133, 162.  4-bit X: 44, 28; 48, 45; 43, 36; 50, 64.
+template <int XT>
+bool big_tiles(const MxArgs &a) {
+    const double big = (double)((a.M + 255) / 256) * (double)((a.N + (XT == 2 ? 191 : 255)) / (XT == 2 ? 192 : 256)) / 256;
+    const double small = (double)((a.M + 63) / 64) * (double)((a.N + 127) / 128) / 256;
+    const double step = XT == 2 ? 2.6 : 2.4 + (big < 1 ? big : 1);
+    return ceil(big) * step < (small > 1 ? small : 1);
+}
+
 template <int XT>
 hipError_t launch_x(const MxArgs &a) {
-    if (a.M > 128) {
-        if constexpr (XT == 2) return launch_t<XT, 2, 4, 8, 3, 2>(a);
-        else return launch_t<XT, 2, 4, 8, 4, 3>(a);   // 256 x 256
-    }
-    if constexpr (XT == 2) return launch_t<XT, 2, 2, 2, 4, 2>(a);                  // 64 x 128
-    else return launch_t<XT, 2, 2, 2, 4, 4>(a);
+    if constexpr (XT == 2) return big_tiles<XT>(a) ? launch_t<XT, 2, 4, 8, 3, 2>(a) : launch_t<XT, 2, 2, 2, 4, 2>(a);
+    else return big_tiles<XT>(a) ? launch_t<XT, 2, 4, 8, 4, 3>(a) : launch_t<XT, 2, 2, 2, 4, 4>(a);
 }
 
 }  // namespace
 
+// Up to 32 rows, tiles have nothing to gain; up to 160, while the rows in sixteens times N stay
+// small, too few tiles to fill the chip take longer than the weights read once for 16 rows.  Measured,
+// K = 5120, us, in sixteens and in tiles: 16-bit X, 128 -> 5120 40 and 45, 64 -> 17408 59 and 49;
+// 4-bit X, 64 -> 5120 18 and 25, 128 -> 5120 27 and 23; 37 x 1056 -> 1001: 4 and 13.
 // Scale bytes are loaded 16 at a time, offsets inside a tile are 32-bit, tiles are counted in an int.
-bool mx_gemm_fits(const MxArgs &a) {
-    const int64_t blocks = a.K / 32;
+bool mx_gemm_wins(const MxArgs &a) {
+    const int64_t blocks = a.K / 32, chunks = (a.M + 15) / 16;
+    if (a.M <= 32 || (chunks <= 10 && chunks * a.N <= (a.x_dtype == 2 ? 32768 : 45056))) return false;
     return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) && ((a.M + 63) / 64) * ((a.N + 63) / 64) < (int64_t(1) << 31);
 }
 

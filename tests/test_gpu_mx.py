@@ -126,7 +126,8 @@ SHAPES = [(1, 1, 32), (1, 5120, 5120), (2, 17, 64), (3, 33, 96), (4, 1000, 1056)
           (7, 300, 4128), (8, 129, 8192), (9, 100, 512), (10, 8, 544), (11, 95, 17408), (12, 7, 640), (13, 130, 32),
           (14, 257, 1024), (15, 64, 2080), (16, 500, 5120), (17, 48, 320), (31, 77, 1184), (33, 40, 768),
           (64, 257, 1056), (65, 300, 2048), (100, 515, 352), (127, 128, 4096), (128, 256, 512), (129, 513, 544),
-          (200, 700, 1312), (257, 1030, 2080), (300, 260, 160), (512, 1024, 1024)]
+          (200, 700, 1312), (257, 1030, 2080), (300, 260, 160), (512, 1024, 1024),
+          (32, 6000, 128), (160, 1111, 96), (161, 300, 2080), (700, 9300, 96), (641, 9411, 544), (1030, 6100, 1056)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
