@@ -230,12 +230,12 @@ def _launch(fn, where: str, t: torch.Tensor, *args) -> None:
         raise TernError(status, where)
 
 
-def _need_at(t: torch.Tensor, name: str, device: torch.device, dtypes, shape) -> None:
-    """t lies on `device`, dense, with one of the types and the shape."""
-    if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
+def _need_at(t: torch.Tensor, name: str, index: int, dtypes, shape) -> None:
+    """t lies on GPU `index` (which is one), dense, with one of the types and the shape."""
+    if t.get_device() == index and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
         return
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the device of the other tensors, {device}; it is on {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the device of the other tensors, cuda:{index}; it is on {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.shape != shape:
@@ -243,25 +243,30 @@ def _need_at(t: torch.Tensor, name: str, device: torch.device, dtypes, shape) ->
     raise ValueError(f"{name} must be contiguous (call .contiguous())")
 
 
-def _need_matrix(t: torch.Tensor, name: str, dtypes) -> None:
+def _need_matrix(t: torch.Tensor, name: str, dtypes) -> int:
+    """t is a dense matrix of one of the types on a GPU, whose index is returned."""
+    index = t.get_device()
+    if index >= 0 and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous():
+        return index
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if not (t.is_cuda and t.dim() == 2 and t.is_contiguous()):
-        _need(t, name, t.dtype)
+    _need(t, name, t.dtype)
+    return index
 
 
 _U8 = (torch.uint8,)
 _F16 = (torch.float16,)
 
 
-def _need_codes(codes: torch.Tensor, exps: torch.Tensor, device: torch.device, prefix: str = ""):
-    """(rows, K) of a matrix held as codes and exps on `device`."""
-    _need_matrix(codes, prefix + "codes", _U8)
+def _need_codes(codes: torch.Tensor, exps: torch.Tensor, index: int, prefix: str = ""):
+    """(rows, K) of a matrix held as codes and exps on GPU `index`."""
+    at = _need_matrix(codes, prefix + "codes", _U8)
     rows, half = codes.shape
     if half % 16 != 0:
         raise ValueError(f"{prefix}codes must be [R, K/2] with K a multiple of 32, got {tuple(codes.shape)}")
-    _need_at(codes, prefix + "codes", device, _U8, (rows, half))
-    _need_at(exps, prefix + "exps", device, _U8, (rows, half // 16))
+    if at != index:
+        _need_at(codes, prefix + "codes", index, _U8, codes.shape)
+    _need_at(exps, prefix + "exps", index, _U8, (rows, half // 16))
     return rows, 2 * half
 
 
@@ -270,9 +275,8 @@ def mx_quantize(x: torch.Tensor):
     power-of-two scale per 32, rounded to nearest even (tern_mx_quantize)."""
     _need_matrix(x, "x", _FLOATS)
     M, K = x.shape
-    device = x.device
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=device)
-    exps = torch.empty((M, K // 32), dtype=torch.uint8, device=device)
+    codes = x.new_empty((M, K // 2), dtype=torch.uint8)
+    exps = x.new_empty((M, K // 32), dtype=torch.uint8)
     _launch(lib.tern_mx_quantize, "tern_mx_quantize", x, x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(),
             exps.data_ptr(), M, K)
     return codes, exps
@@ -281,13 +285,13 @@ def mx_quantize(x: torch.Tensor):
 def mx_dequant(codes: torch.Tensor, exps: torch.Tensor, out_dtype: torch.dtype = torch.float32,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values [M,K] of a matrix held as codes and exps; exact in fp32 and bf16."""
-    M, K = _need_codes(codes, exps, codes.device)
+    M, K = _need_codes(codes, exps, codes.get_device())
     if out is None:
         if out_dtype not in _TORCH_CODE:
             raise TypeError("out_dtype must be float32, bfloat16 or float16")
         out = torch.empty((M, K), dtype=out_dtype, device=codes.device)
     else:
-        _need_at(out, "out", codes.device, _FLOATS, (M, K))
+        _need_at(out, "out", codes.get_device(), _FLOATS, (M, K))
     _launch(lib.tern_mx_dequant, "tern_mx_dequant", codes, codes.data_ptr(), exps.data_ptr(), out.data_ptr(),
             _TORCH_CODE[out.dtype], M, K)
     return out
@@ -295,12 +299,12 @@ def mx_dequant(codes: torch.Tensor, exps: torch.Tensor, out_dtype: torch.dtype =
 
 def mx_matmul_into(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
     """out[M,N] = x[M,K] . W^T, x fp16/bf16, W [N,K] held as codes and exps."""
-    _need_matrix(x, "x", _FLOAT16S)
-    N, K = _need_codes(codes, exps, x.device)
-    M = x.shape[0]
-    if x.shape[1] != K:
+    index = _need_matrix(x, "x", _FLOAT16S)
+    N, K = _need_codes(codes, exps, index)
+    M, KX = x.shape
+    if KX != K:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, codes {tuple(codes.shape)}")
-    _need_at(out, "out", x.device, _FLOATS, (M, N))
+    _need_at(out, "out", index, _FLOATS, (M, N))
     _launch(lib.tern_mx_matmul, "tern_mx_matmul", x, x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(),
             exps.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K)
     return out
@@ -309,18 +313,19 @@ def mx_matmul_into(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, out
 def mx_matmul(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
               out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Y[M,N] = x[M,K] . W^T with fp32 accumulation, W [N,K] held as codes and exps; returns a new tensor."""
-    out = torch.empty((x.shape[0], codes.shape[0]), dtype=out_dtype, device=x.device)
+    out = x.new_empty((x.shape[0], codes.shape[0]), dtype=out_dtype)
     return mx_matmul_into(x, codes, exps, out)
 
 
 def mx_matmul_mx_into(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
                       out: torch.Tensor) -> torch.Tensor:
     """out[M,N] = X . W^T with both matrices held as codes and exps."""
-    M, K = _need_codes(x_codes, x_exps, x_codes.device, "x_")
-    N, KW = _need_codes(codes, exps, x_codes.device)
+    index = x_codes.get_device()
+    M, K = _need_codes(x_codes, x_exps, index, "x_")
+    N, KW = _need_codes(codes, exps, index)
     if K != KW:
         raise ValueError(f"shape mismatch: x_codes {tuple(x_codes.shape)}, codes {tuple(codes.shape)}")
-    _need_at(out, "out", x_codes.device, _FLOATS, (M, N))
+    _need_at(out, "out", index, _FLOATS, (M, N))
     _launch(lib.tern_mx_matmul_mx, "tern_mx_matmul_mx", x_codes, x_codes.data_ptr(), x_exps.data_ptr(),
             codes.data_ptr(), exps.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K)
     return out
@@ -329,7 +334,7 @@ def mx_matmul_mx_into(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.
 def mx_matmul_mx(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
                  out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Y[M,N] = X . W^T with both matrices held as codes and exps; returns a new tensor."""
-    out = torch.empty((x_codes.shape[0], codes.shape[0]), dtype=out_dtype, device=x_codes.device)
+    out = x_codes.new_empty((x_codes.shape[0], codes.shape[0]), dtype=out_dtype)
     return mx_matmul_mx_into(x_codes, x_exps, codes, exps, out)
 
 
@@ -340,14 +345,13 @@ def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_
              renormalize: bool = True, group: int = 128) -> torch.Tensor:
     """out [T,H] = the mixture-of-experts layer of tern_moe: x [T,H] fp16/bf16, logits [T,E],
     gate_up [E,2F,H/4] and down [E,H,F/4] packed codes, their fp16 scales one per 128."""
-    _need_matrix(x, "x", _FLOAT16S)
+    device = _need_matrix(x, "x", _FLOAT16S)
     if gate_up.dim() != 3 or down.dim() != 3:
         raise ValueError("gate_up must be [E, 2F, H/4] and down [E, H, F/4]")
     if group <= 0:
         raise ValueError("group must be positive")
     T, H = x.shape
     E, F = gate_up.shape[0], down.shape[2] * 4
-    device = x.device
     _need_at(logits, "logits", device, _FLOATS, (T, E))
     _need_at(gate_up, "gate_up", device, _U8, (E, 2 * F, H // 4))
     _need_at(gate_up_scales, "gate_up_scales", device, _F16, (E, 2 * F, H // group))
@@ -357,7 +361,7 @@ def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_
     nbytes = lib.tern_moe_workspace(T, E, top_k, H, F)
     # allocated on the current stream: torch's allocator keeps it for this call until that stream
     # has passed it, and inside a graph capture it belongs to the graph
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    ws = x.new_empty((nbytes,), dtype=torch.uint8)
     _launch(lib.tern_moe, "tern_moe", x, x.data_ptr(), _TORCH_CODE[x.dtype], logits.data_ptr(),
             _TORCH_CODE[logits.dtype], gate_up.data_ptr(), gate_up_scales.data_ptr(), down.data_ptr(),
             down_scales.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], T, E, top_k, H, F, group,
@@ -369,7 +373,7 @@ def moe(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_sc
         down: torch.Tensor, down_scales: torch.Tensor, top_k: int, renormalize: bool = True,
         out_dtype: Optional[torch.dtype] = None, group: int = 128) -> torch.Tensor:
     """The layer's outputs [T,H] (of x's type unless out_dtype is given) as a new tensor."""
-    out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    out = x.new_empty(x.shape, dtype=out_dtype)
     return moe_into(x, logits, gate_up, gate_up_scales, down, down_scales, out, top_k, renormalize, group)
 
 
