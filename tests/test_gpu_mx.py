@@ -122,6 +122,14 @@ def nan_out(M, N, yd):
 
 
 # every M from 1 to 17 somewhere, one block to many steps, N of one row, off the tiles
+@pytest.mark.parametrize("M,K,yd", [(4200, 4096, "bf16"), (4201, 4160, "f32"), (5000, 4128, "f16")])
+def test_dequant_past_the_caches(M, K, yd):
+    print(f"mx_dequant {M}x{K} -> {yd}", flush=True)
+    codes, exps = weights(M, K, M + K, spread=6)
+    y = tern.mx_dequant(dev(codes), dev(exps), DT[yd])
+    assert torch.equal(y.cpu(), torch.from_numpy(np.asarray(R.values(codes, exps))).to(DT[yd]))
+
+
 SHAPES = [(1, 1, 32), (1, 5120, 5120), (2, 17, 64), (3, 33, 96), (4, 1000, 1056), (5, 16, 256), (6, 31, 288),
           (7, 300, 4128), (8, 129, 8192), (9, 100, 512), (10, 8, 544), (11, 95, 17408), (12, 7, 640), (13, 130, 32),
           (14, 257, 1024), (15, 64, 2080), (16, 500, 5120), (17, 48, 320), (31, 77, 1184), (33, 40, 768),
