@@ -673,7 +673,7 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(Plan plan, void *__restric
 // (expert, step) units in turn; the slots of the tiles are the tokens, and one that did not take
 // the expert at hand has zeros there.
 template <int SETS, int Q>
-__global__ __launch_bounds__(768) void moe_down_small_kernel(const uint8_t *__restrict__ D,
+__global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__restrict__ D,
                                                             const uint16_t *__restrict__ DS, Plan plan,
                                                             void *__restrict__ Y, int y_dtype, int T, int E, int top_k,
                                                             int H, int F, int nw) {
@@ -843,7 +843,7 @@ hipError_t launch_down(const MoeArgs &a, const Plan &plan, int slots) {
 template <int SETS, int Q>
 hipError_t launch_down_small(const MoeArgs &a, const Plan &plan) {
     const int64_t units = a.T * a.top_k * ((a.F + 511) / 512);   // at most
-    const int nw = (int)(units < 12 ? units : 12);
+    const int nw = (int)(units < 8 ? units : 8);
     const dim3 g((unsigned)((a.H + 4 * Q - 1) / (4 * Q))), b(64 * nw);
     const size_t lds = (size_t)nw * sums_floats<SETS, Q>() * 4 + kMoeSmall * kMoeMaxTopK * 4 * (2 + kMoeSmall) +
                        kMoeMaxExperts / 8 + 4;
@@ -855,12 +855,14 @@ hipError_t launch_down_small(const MoeArgs &a, const Plan &plan) {
     return hipGetLastError();
 }
 
-// Steps of K that come in twos rather than in fours.
+// Steps of K that come in twos rather than in fours.  The up kernel takes them so, with twice the rows
+// a wave, only if that leaves every SIMD two waves (one token, 2 experts of 5120 x 2048: 21.7 us for
+// the layer with them, 18.6 without; four tokens, 8 experts: 32.8 and 34.8).
 bool few_steps(int64_t K) { return (K + 511) / 512 % 4 == 1 || (K + 511) / 512 % 4 == 2; }
 
 template <int SETS, bool SMALL>
 hipError_t up(const MoeArgs &a, const Plan &plan, int slots) {
-    if (few_steps(a.H))
+    if (few_steps(a.H) && a.F / 8 * slots >= 2048)
         return a.x_dtype == 0 ? launch_up<0, SETS, 4, 2, SMALL>(a, plan, slots) : launch_up<1, SETS, 4, 2, SMALL>(a, plan, slots);
     return a.x_dtype == 0 ? launch_up<0, SETS, 2, 4, SMALL>(a, plan, slots) : launch_up<1, SETS, 2, 4, SMALL>(a, plan, slots);
 }
