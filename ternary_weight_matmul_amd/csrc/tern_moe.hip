@@ -31,17 +31,17 @@
 // first are on their way before the activations are fetched.
 //   With K split over the waves instead, sums met in LDS once a block of rows,
 // each behind a barrier: 107 us for both products at 32 tokens of the sizes
-// below, against 62.
+// below, against 58.
 //
-// Bound: HBM for one token (the codes of the experts that are taken, once for
-// all of their tokens: E = 64, k = 8, 2048 x 1024: 12.6 MB, 14 us with both
-// launches, of which routing, first loads and launches are about 8).  At 32
-// tokens (97 MB) decoding the codes, 36 vector instructions a quad and step,
-// and the 8 matrix instructions they feed: 33 + 29 us, and 7 + 5 for the plan
-// and the sum.
+// Bound: latency for one token (E = 64, k = 8, 2048 x 1024: 12.6 MB of codes,
+// 3.7 us for a plain read; up 8.1 us, routing first, and down 5.8).  At 32
+// tokens (97 MB, 16 us) decoding the codes, 36 vector instructions a quad and
+// step, and the 4 or 8 matrix instructions they feed: 30 + 28 us, and 7 + 5
+// for the plan and the sum.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tern_device.h"
 #include "tern_launch.h"
@@ -557,8 +557,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
         e = uniform(plan.experts[blockIdx.y]);
     }
     const int units = (F + 2 * Q - 1) / (2 * Q);
-    for (int base = 0; base < count; base += ROWS) {
-        product<AT, SETS, Q, G>(
+    int base = 0;
+    auto go = [&](auto sets) __attribute__((always_inline)) {
+        constexpr int S = decltype(sets)::value, ROWS = S * rows_per_set(AT);
+        product<AT, S, Q, G>(
             [&]() __attribute__((always_inline)) {
                 if constexpr (!SMALL) {
                     if (base > 0) __syncthreads();   // the operands of the chunk before are read
@@ -569,7 +571,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
                         rowweight[tid] = pr >= 0 ? plan.weights[pr] : 0.f;
                     }
                     __syncthreads();
-                    stage<SETS>(ops, X, off, groups, tid, 64 * kWaves);
+                    stage<S>(ops, X, off, groups, tid, 64 * kWaves);
                     __syncthreads();
                 }
             },
@@ -583,11 +585,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
 #pragma unroll
                 for (int o0 = 0; o0 < ROWS * 2 * Q; o0 += 64) {
                     const int o = o0 + lane, ff = o % (2 * Q), i = min(o / (2 * Q), ROWS - 1), f = u * 2 * Q + ff;
-                    const float g = sum_of<SETS>(sm, i / 4, ff / 4, i % 4, ff % 4);
-                    const float y = sum_of<SETS>(sm, i / 4, ff / 4 + Q / 2, i % 4, ff % 4);
+                    const float g = sum_of<S>(sm, i / 4, ff / 4, i % 4, ff % 4);
+                    const float y = sum_of<S>(sm, i / 4, ff / 4 + Q / 2, i % 4, ff % 4);
                     const int pr = rowpair[i];
                     const float h = g / (1.f + expf(-g)) * y * rowweight[i];
-                    const __bf16 hi = (__bf16)h, lo = (__bf16)(__builtin_isinf((float)hi) ? 0.f : h - (float)hi);   // infinity has no rest
+                    const __bf16 hi = (__bf16)h;
+                    const __bf16 lo = (__bf16)(__builtin_isinf((float)hi) ? 0.f : h - (float)hi);   // infinity has no rest
                     if (o < ROWS * 2 * Q && pr >= 0 && f < F) {
                         uint16_t *at = plan.hid + (int64_t)pr * hid_words(F) + hidden_at(f);
                         at[0] = __builtin_bit_cast(uint16_t, hi);
@@ -595,6 +598,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
                     }
                 }
             });
+        base += ROWS;
+    };
+    while (base < count) {   // one set will do for a few tokens (32 tokens: 33 -> 30 us, down 29 -> 28)
+        if (SETS > 1 && count - base <= rows_per_set(AT)) go(std::integral_constant<int, 1>());
+        else go(std::integral_constant<int, SETS>());
     }
 }
 
@@ -614,13 +622,15 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t 
     if (count <= 0) return;
     const int e = uniform(plan.experts[blockIdx.y]);
     const int units = (H + 4 * Q - 1) / (4 * Q);
-    for (int base = 0; base < count; base += ROWS) {
-        product<2, SETS, Q, G>(
+    int base = 0;
+    auto go = [&](auto sets) __attribute__((always_inline)) {
+        constexpr int S = decltype(sets)::value, ROWS = S * rows_per_set(2);
+        product<2, S, Q, G>(
             [&]() __attribute__((always_inline)) {
                 if (base > 0) __syncthreads();   // the operands of the chunk before are read
                 if (tid < ROWS) rowpair[tid] = base + tid < count ? plan.pairs[start + base + tid] : -1;
                 __syncthreads();
-                stage_hidden<SETS>(ops, plan.hid, rowpair, groups, tid, 64 * kWaves);
+                stage_hidden<S>(ops, plan.hid, rowpair, groups, tid, 64 * kWaves);
                 __syncthreads();
             },
             ops, sums + wave * sums_floats<SETS, Q>(), blockIdx.x * kWaves + wave, gridDim.x * kWaves, units, groups, lane,
@@ -633,12 +643,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t 
 #pragma unroll
                 for (int o0 = 0; o0 < ROWS * 4 * Q; o0 += 64) {
                     const int o = o0 + lane, nn = o % (4 * Q), i = min(o / (4 * Q), ROWS - 1), n = u * 4 * Q + nn;
-                    const float y = sum_of<SETS>(sm, i / 2, nn / 4, i % 2, nn % 4) +
-                                    sum_of<SETS>(sm, i / 2, nn / 4, i % 2 + 2, nn % 4);
+                    const float y = sum_of<S>(sm, i / 2, nn / 4, i % 2, nn % 4) +
+                                    sum_of<S>(sm, i / 2, nn / 4, i % 2 + 2, nn % 4);
                     const int pr = rowpair[i];
                     if (o < ROWS * 4 * Q && pr >= 0 && n < H) plan.part[(int64_t)pr * H + n] = y;
                 }
             });
+        base += ROWS;
+    };
+    while (base < count) {
+        if (SETS > 1 && count - base <= rows_per_set(2)) go(std::integral_constant<int, 1>());
+        else go(std::integral_constant<int, SETS>());
     }
 }
 

@@ -153,8 +153,9 @@ hipError_t dequant(const uint32_t *codes, const uint8_t *exps, void *W, int64_t 
 hipError_t launch_mx_dequant(const uint8_t *codes, const uint8_t *exps, void *W, int w_dtype, int64_t blocks,
                              hipStream_t stream) {
     const uint32_t *c = reinterpret_cast<const uint32_t *>(codes);
-    return w_dtype == 0 ? dequant<0>(c, exps, W, blocks * 4, stream)
-                        : (w_dtype == 1 ? dequant<1>(c, exps, W, blocks * 4, stream) : dequant<2>(c, exps, W, blocks * 4, stream));
+    const int64_t octets = blocks * 4;
+    if (w_dtype == 0) return dequant<0>(c, exps, W, octets, stream);
+    return w_dtype == 1 ? dequant<1>(c, exps, W, octets, stream) : dequant<2>(c, exps, W, octets, stream);
 }
 
 }  // namespace tern

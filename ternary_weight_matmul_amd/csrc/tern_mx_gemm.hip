@@ -443,7 +443,8 @@ hipError_t launch_x(const MxArgs &a) {
 bool mx_gemm_wins(const MxArgs &a) {
     const int64_t blocks = a.K / 32, chunks = (a.M + 15) / 16;
     if (a.M <= 32 || (chunks <= 10 && chunks * a.N <= (a.x_dtype == 2 ? 32768 : 45056))) return false;
-    return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) && ((a.M + 63) / 64) * ((a.N + 63) / 64) < (int64_t(1) << 31);
+    return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) &&
+           ((a.M + 63) / 64) * ((a.N + 63) / 64) < (int64_t(1) << 31);
 }
 
 hipError_t launch_mx_gemm(const MxArgs &a) {
