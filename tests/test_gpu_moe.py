@@ -230,6 +230,29 @@ def test_streams_and_graph_replays(T):
             assert torch.equal(y, want[(i + j) % 4])
 
 
+@pytest.mark.parametrize("T", [1, 6])
+def test_experts_past_32_bits(T):
+    """The last of 40 experts, whose rows start 5 GB into the weights, gives the bits it gives alone."""
+    E, H, F = 40, 16384, 16384
+    print(f"moe T={T} E={E} H={H} F={F}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    codes = [torch.zeros((E, 2 * F, H // 4), dtype=torch.uint8, device=DEV),
+             torch.zeros((E, H, F // 4), dtype=torch.uint8, device=DEV)]
+    scales = [torch.zeros((E, 2 * F, H // 128), dtype=torch.float16, device=DEV),
+              torch.zeros((E, H, F // 128), dtype=torch.float16, device=DEV)]
+    for c, s in zip(codes, scales):
+        c[-1].copy_(torch.randint(0, 256, c[-1].shape, dtype=torch.uint8, device=DEV, generator=g))
+        s[-1].fill_(2.0 ** -7)
+    x = torch.randn((T, H), device=DEV, generator=g).to(torch.bfloat16)
+    lg = torch.full((T, E), -float("inf"), device=DEV)
+    lg[:, -1] = 0.5
+    y = tern.moe(x, lg, codes[0], scales[0], codes[1], scales[1], 1, out_dtype=torch.float32)
+    one = tern.moe(x, lg[:, -1:].contiguous(), codes[0][-1:].contiguous(), scales[0][-1:].contiguous(),
+                   codes[1][-1:].contiguous(), scales[1][-1:].contiguous(), 1, out_dtype=torch.float32)
+    assert torch.isfinite(y).all() and y.abs().max() > 0
+    assert torch.equal(y, one)
+
+
 def test_refusals():
     E, H, F = 4, 256, 128
     L = Layer(E, H, F, 15)

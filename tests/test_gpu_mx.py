@@ -292,6 +292,31 @@ def test_misaligned_and_strided_inputs_are_refused():
         tern.mx_matmul(x[:, :64].contiguous(), codes, exps.cpu())
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 130, 1024), (7, 33, 1056), (40, 700, 2048), (200, 301, 352), (641, 9411, 96)])
+@pytest.mark.parametrize("kind", ["bf16", "mx"])
+def test_scales_and_outputs_at_any_address(M, N, K, kind):
+    """Exponent bytes at an odd address and outputs at an odd element give the same bits."""
+    print(f"addresses {M}x{K}->{N} {kind}", flush=True)
+    codes, exps = (dev(t) for t in weights(N, K, M + K))
+    xc, xe = (dev(t) for t in weights(M, K, M + N, spread=4))
+    x = activations(M, K, "bf16", M).to(DEV)
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:]
+        flat.copy_(t.reshape(-1))
+        return flat.view(t.shape)
+
+    def product(ex, xex, out):
+        return (tern.mx_matmul_into(x, codes, ex, out) if kind == "bf16"
+                else tern.mx_matmul_mx_into(xc, xex, codes, ex, out))
+
+    for yd in (torch.bfloat16, torch.float32):
+        want = product(exps, xe, torch.empty((M, N), dtype=yd, device=DEV))
+        got = product(shifted(exps), shifted(xe), shifted(torch.zeros((M, N), dtype=yd, device=DEV)))
+        assert torch.equal(got, want)
+    assert torch.equal(tern.mx_dequant(codes, shifted(exps)), tern.mx_dequant(codes, exps))
+
+
 def test_empty_sizes():
     e = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
     c, s = tern.mx_quantize(e)
