@@ -870,6 +870,24 @@ hipError_t launch_down_small(const MoeArgs &a, const Plan &plan) {
     return hipGetLastError();
 }
 
+// Rows of a workgroup of the small down kernel: one workgroup a CU where they allow it, else few
+// rounds of them (four tokens, H = 5120: 16, 24, 32 rows 13.9, 9.4, 10.9 us; H = 2048: 16 rows 2 us
+// more than 8).
+template <int SETS>
+hipError_t down_small(const MoeArgs &a, const Plan &plan) {
+    int best = 0, least = 0;
+    for (int q = 2; q <= 8; q += 2) {
+        const int cost = (int)(((a.H + 4 * q - 1) / (4 * q) + 255) / 256) * (q + 1);
+        if (best == 0 || cost < least) least = cost, best = q;
+    }
+    switch (best) {
+    case 2: return launch_down_small<SETS, 2>(a, plan);
+    case 4: return launch_down_small<SETS, 4>(a, plan);
+    case 6: return launch_down_small<SETS, 6>(a, plan);
+    default: return launch_down_small<SETS, 8>(a, plan);
+    }
+}
+
 // Steps of K that come in twos rather than in fours.  The up kernel takes them so, with twice the rows
 // a wave, only if that leaves every SIMD two waves (one token, 2 experts of 5120 x 2048: 21.7 us for
 // the layer with them, 18.6 without; four tokens, 8 experts: 32.8 and 34.8).
@@ -890,9 +908,7 @@ hipError_t launch_chunk(const MoeArgs &a) {
     if (a.T <= kMoeSmall) {
         e = up<1, true>(a, plan, slots);
         if (e != hipSuccess) return e;
-        // More rows a workgroup once they fill the chip all the same (T = 4: H = 5120, 17.3 -> 15.2 us; H = 2048, 5 -> 7)
-        if (a.T <= 2) return launch_down_small<1, 2>(a, plan);
-        return a.H < 4096 ? launch_down_small<2, 2>(a, plan) : launch_down_small<2, 4>(a, plan);
+        return a.T <= 2 ? down_small<1>(a, plan) : down_small<2>(a, plan);
     }
     hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.logits, a.l_dtype, (int)a.T, (int)a.E,
                        (int)a.top_k, a.renormalize, slots, plan);

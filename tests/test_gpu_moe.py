@@ -62,7 +62,8 @@ SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 256, 128), (1, 64, 8, 1024, 512), (2, 5
           (4, 8, 2, 2176, 256), (5, 16, 8, 384, 640), (7, 3, 1, 512, 1152), (8, 32, 4, 1280, 128), (9, 2, 2, 256, 256),
           (16, 60, 6, 512, 384), (17, 9, 5, 128, 128), (33, 100, 7, 384, 256), (64, 4, 2, 256, 128),
           (65, 6, 2, 256, 256), (130, 5, 1, 128, 256), (2, 130, 32, 128, 128), (1, 1024, 32, 128, 128),
-          (1, 4, 2, 8704, 128), (6, 3, 2, 128, 8832)]
+          (1, 4, 2, 8704, 128), (6, 3, 2, 128, 8832), (4, 4, 2, 5120, 256), (3, 3, 2, 6272, 128), (2, 4, 2, 5248, 384),
+          (4, 3, 1, 4096, 640)]
 
 
 @pytest.mark.parametrize("T,E,k,H,F", SHAPES)
