@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "tern_buffer.h"
 #include "tern_device.h"
 #include "tern_launch.h"
 #include "tern_moe.h"
@@ -54,17 +55,6 @@ namespace {
 typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4v_t __attribute__((ext_vector_type(4)));
-
-constexpr int OUT_OF_RANGE = (int)0x80000000;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
-}
-
-__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, int off, int at) {
-    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, at, 0)));
-}
 
 // What every lane holds, in a scalar register: a buffer descriptor made from anything else is
 // gathered lane by lane in a loop around each load.
@@ -294,11 +284,9 @@ __device__ __forceinline__ At place_of(int s, int groups, int lane, bool live) {
 
 template <int Q>
 __device__ __forceinline__ void load_quad(Step<Q> &st, const Rows &w, const At &at, int groups, int q) {
-    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-    st.scale[q] = __builtin_amdgcn_raw_buffer_load_b16(q < Q / 2 ? w.sa : w.sb, at.scale, 4 * (q % (Q / 2)) * groups * 2, 0);
-    const u32x2 v = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_raw_buffer_load_b64(q < Q / 2 ? w.a : w.b, at.code, 4 * (q % (Q / 2)) * groups * 32, 2));
-    st.code[q] = make_uint2(v[0], v[1]);
+    const int row = 4 * (q % (Q / 2)) * groups;
+    st.scale[q] = __builtin_amdgcn_raw_buffer_load_b16(q < Q / 2 ? w.sa : w.sb, at.scale + row * 2, 0, 0);
+    st.code[q] = load8<2>(q < Q / 2 ? w.a : w.b, at.code + row * 32);
 }
 
 // Activations of the tiles' rows into LDS: operand i of set t of step s at ((s SETS + t) 4 + i) KB,
@@ -747,7 +735,7 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
             const int tok = 2 * t + (slot & 1), pr = live && tok < T ? pair[i * T + min(tok, T - 1)] : -1;
             const int off = pr >= 0 && 4 * s + ca < groups ? pr * per_pair + s * 2048 + lane_at : OUT_OF_RANGE;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a[t][k] = load16(rx, off, k * 256);
+            for (int k = 0; k < 4; ++k) a[t][k] = load16(rx, off + k * 256);
         }
         const int64_t r0 = (int64_t)e * H + n0;
         w = rows_of(D, DS, r0, r0 + 2 * Q, min(2 * Q, H - n0), min(2 * Q, H - n0 - 2 * Q), groups);

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "tern_buffer.h"
 #include "tern_device.h"
 #include "tern_launch.h"
 

@@ -61,17 +61,6 @@ __device__ __forceinline__ int swz(int row, int c) {
 // Lambdas of the kernel: left as calls, their captures live in scratch memory.
 #define TERN_INLINE __attribute__((always_inline))
 
-constexpr int OUT_OF_RANGE = (int)0x80000000;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t *base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0, bytes, 0x00020000);
-}
-
-// Lane l's 16 bytes at r[off + at] -> lds + 16 l; zeros where that is out of range.
-__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t *lds, int off, int at) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, off, at, 0, 0);
-}
-
 // At most LATER loads of this wave are still on their way, its LDS accesses are done, and every
 // wave of the workgroup has got here.  In one piece: __syncthreads would wait for every load.
 template <int LATER>
@@ -160,8 +149,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
 
     const int xrow = blocks * (T::MX ? 16 : 64), wrow = blocks * 16;
     const int xrows = min(T::BM, M - m0), wrows = min(T::BN, N - n0);
-    const __amdgpu_buffer_rsrc_t rx = rows_of(X + (int64_t)m0 * xrow, xrows * xrow);
-    const __amdgpu_buffer_rsrc_t rw = rows_of(W + (int64_t)n0 * wrow, wrows * wrow);
+    const __amdgpu_buffer_rsrc_t rx = buffer_of(X + (int64_t)m0 * xrow, xrows * xrow);
+    const __amdgpu_buffer_rsrc_t rw = buffer_of(W + (int64_t)n0 * wrow, wrows * wrow);
     const int steps = (blocks + T::BPS - 1) / T::BPS;
 
     // Tiles go from memory straight to LDS, 16 bytes a lane, 1 KB an instruction.  Rows past the
@@ -174,15 +163,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
     const int aoff = ar * xrow + ac * 16, woff = wr * wrow + wc * 16;
     auto fetch = [&](uint8_t *to, int s) TERN_INLINE {
         const int left = blocks - s * T::BPS;   // blocks of this step
-        const int ao = ac < left * (T::MX ? 1 : 4) ? aoff : OUT_OF_RANGE;
-        const int wo = wc < left ? woff : OUT_OF_RANGE;
+        const int ao = (ac < left * (T::MX ? 1 : 4) ? aoff : OUT_OF_RANGE) + s * T::XROW;
+        const int wo = (wc < left ? woff : OUT_OF_RANGE) + s * T::WROW;
 #pragma unroll
         for (int i = 0; i < T::AI; ++i)
-            to_lds(rx, to + (i * T::WAVES + wave) * 1024, ao, i * T::WAVES * (64 / XL) * xrow + s * T::XROW);
+            load16_to_lds(rx, to + (i * T::WAVES + wave) * 1024, ao + i * T::WAVES * (64 / XL) * xrow);
 #pragma unroll
         for (int i = 0; i < T::WI; ++i)
-            to_lds(rw, to + T::A_LDS + (i * T::WAVES + wave) * 1024, wo,
-                   i * T::WAVES * (64 / WL) * wrow + s * T::WROW);
+            load16_to_lds(rw, to + T::A_LDS + (i * T::WAVES + wave) * 1024, wo + i * T::WAVES * (64 / WL) * wrow);
     };
 
     // With 4-bit X a step is short and its tiles come late: every line is new to the XCD's L2.  So
@@ -195,8 +183,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(const uint8_t *__
     const int toff = lane < (tx ? T::BM / 4 : T::BN / 8) ? (tshare + lane) * (tx ? xrow : wrow) : OUT_OF_RANGE;
     auto touch = [&](int s) TERN_INLINE {
         if (T::MX && wave < 2 && s < steps)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rt, (__attribute__((address_space(3))) void *)(touched + wave * 256), 4, toff, s * T::XROW, 0, 0);
+            load4_to_lds(rt, touched + wave * 256, toff + s * T::XROW);
     };
 
     // Scale bytes go through registers, 16 of a row at a time (512 values): a load costs a request

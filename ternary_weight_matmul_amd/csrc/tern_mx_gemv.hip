@@ -50,18 +50,6 @@ namespace {
 typedef float float4v_t __attribute__((ext_vector_type(4)));
 typedef int int8v_t __attribute__((ext_vector_type(8)));
 
-constexpr int OUT_OF_RANGE = (int)0x80000000;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
-}
-
-template <int NT = 0>   // 2: non-temporal, for bytes that are read once
-__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, int off, int at) {
-    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(uint4, __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, at, NT)));
-}
-
 // The place of 16-byte chunk c (0..31) of activation row t in a wave's corner.  Lanes that are
 // served together read two chunks 4 apart of each of 8 rows: XORed with these they fall on 16
 // distinct places of 256 bytes.
@@ -136,28 +124,28 @@ __global__ __launch_bounds__(64 * kMaxWaves) void mx_gemv_kernel(
             for (int t = 0; t < SETS; ++t) {
                 const int at = (8 * t + as) * blocks + ab;
                 const bool ok = mine && ab < blocks && 8 * t + as < xrows;
-                st.x[t] = load16(rx, ok ? at * 16 : OUT_OF_RANGE, 0);
+                st.x[t] = load16(rx, ok ? at * 16 : OUT_OF_RANGE);
                 st.xscale[t] = __builtin_amdgcn_raw_buffer_load_b8(rxe, ok ? at : OUT_OF_RANGE, 0, 0);
             }
         } else {
             const int chunk = 32 * s + (lane & 31);   // 8 activations
             const int off = mine && chunk < 4 * blocks ? (lane >> 5) * xrow + chunk * 16 : OUT_OF_RANGE;
 #pragma unroll
-            for (int i = 0; i < T::XL; ++i) st.x[i] = load16(rx, off, 2 * i * xrow);
+            for (int i = 0; i < T::XL; ++i) st.x[i] = load16(rx, off + 2 * i * xrow);
         }
     };
     auto load_group = [&](S &st, int s, int b) __attribute__((always_inline)) {
         const int wb = 8 * s + 4 * c + p;   // this lane's block
         const int at = s < last && wb < blocks ? r * blocks + wb : OUT_OF_RANGE;
-        if constexpr (!SC4) st.scale[b] = __builtin_amdgcn_raw_buffer_load_b8(re, at, 8 * b * blocks, 0);
-        st.code[b] = load16<NT>(rw, at < 0 ? OUT_OF_RANGE : at * 16, 8 * b * blocks * 16);
+        if constexpr (!SC4) st.scale[b] = __builtin_amdgcn_raw_buffer_load_b8(re, at + 8 * b * blocks, 0, 0);
+        st.code[b] = load16<NT>(rw, (at < 0 ? OUT_OF_RANGE : at * 16) + 8 * b * blocks * 16);
     };
     // Scale bytes of steps s .. s + 3: lane (u, 2 r + c) holds the 4 of half c of step s + u, row r.
     auto load_scales = [&](uint32_t (&sc)[NB], int s) __attribute__((always_inline)) {
         const int at = 8 * (s + p) + 4 * c;
         const int off = at < blocks ? r * blocks + at : OUT_OF_RANGE;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) sc[b] = __builtin_amdgcn_raw_buffer_load_b32(re, off, 8 * b * blocks, 0);
+        for (int b = 0; b < NB; ++b) sc[b] = __builtin_amdgcn_raw_buffer_load_b32(re, off + 8 * b * blocks, 0, 0);
     };
     // Computes step s (the u-th of its four) and refills what it has used with step s + 1.
     auto step = [&](S &st, const uint32_t (&sc)[NB], int s, int u) __attribute__((always_inline)) {
