@@ -353,9 +353,14 @@ __device__ __forceinline__ void stage_tokens(char *ops, const char *x, int T, in
     }
 }
 
-// acc[t] += scale * (codes . a[t]) for one quad.
-template <int AT, int SETS>
-__device__ __forceinline__ void quad(uint2 code, uint32_t scale_bits, const uint4 (&a)[SETS][4], float4v_t (&acc)[SETS]) {
+struct EverySlot {
+    __device__ __forceinline__ bool operator()(int, int) const { return true; }
+};
+
+// acc[t] += scale * (codes . a[t]) for one quad, in the slots (t, i) that takes() holds for.
+template <int AT, int SETS, typename Takes = EverySlot>
+__device__ __forceinline__ void quad(uint2 code, uint32_t scale_bits, const uint4 (&a)[SETS][4], float4v_t (&acc)[SETS],
+                                     Takes takes = Takes()) {
     const uint64_t v = sign_nz_fields64<true>((uint64_t)code.x | ((uint64_t)code.y << 32));
     uint32_t l[8], h[8];
     weight_pairs2<0, true>(v, l[0], h[0]);
@@ -375,7 +380,7 @@ __device__ __forceinline__ void quad(uint2 code, uint32_t scale_bits, const uint
 #pragma unroll
         for (int i = 0; i < 4; ++i) d = mfma16<AT>(a[t][i], b[i], d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(scale, d[i], acc[t][i]);
+        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(takes(t, i) ? scale : 0.f, d[i], acc[t][i]);
     }
 }
 
@@ -673,8 +678,8 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(Plan plan, void *__restric
 }
 
 // Few tokens: a workgroup goes through every taken expert for its rows of Y.  Its waves take the
-// (expert, step) units in turn; the slots of the tiles are the tokens, and one that did not take
-// the expert at hand has zeros there.
+// (expert, step) units in turn; the slots of the tiles are the tokens.  One that did not take the
+// expert at hand has zeros there, and zeros in place of the expert's scales: they need not be finite.
 template <int SETS, int Q>
 __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__restrict__ D,
                                                             const uint16_t *__restrict__ DS, Plan plan,
@@ -723,6 +728,7 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
     const int lane_at = (slot >> 1) * 1024 + (ca * 4 + (lane >> 4)) * 16;   // in a step's 2 KB
 
     uint4 a[SETS][4];
+    uint64_t took[SETS];   // bit of a slot's lane: its token took the unit's expert
     Step<Q> st;
     Rows w;
     At at;
@@ -733,6 +739,7 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
 #pragma unroll
         for (int t = 0; t < SETS; ++t) {
             const int tok = 2 * t + (slot & 1), pr = live && tok < T ? pair[i * T + min(tok, T - 1)] : -1;
+            took[t] = __ballot(pr >= 0);
             const int off = pr >= 0 && 4 * s + ca < groups ? pr * per_pair + s * 2048 + lane_at : OUT_OF_RANGE;
 #pragma unroll
             for (int k = 0; k < 4; ++k) a[t][k] = load16(rx, off + k * 256);
@@ -750,14 +757,17 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
         for (int q = 0; q < Q; ++q) load_quad<Q>(st, w, at, groups, q);
         for (;;) {
             uint4 now[SETS][4];
+            uint64_t takers[SETS];
 #pragma unroll
-            for (int t = 0; t < SETS; ++t)
+            for (int t = 0; t < SETS; ++t) {
+                takers[t] = took[t];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) now[t][k] = a[t][k];
+            }
             fetch(u + nw);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                quad<2, SETS>(st.code[q], st.scale[q], now, acc[q]);
+                quad<2, SETS>(st.code[q], st.scale[q], now, acc[q], [&](int t, int i) { return (takers[t] >> i & 1) != 0; });
                 load_quad<Q>(st, w, at, groups, q);
                 __builtin_amdgcn_sched_barrier(0);
             }
