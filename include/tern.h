@@ -280,7 +280,11 @@ tern_status tern_mx_matmul_mx(const uint8_t *x_codes, const uint8_t *x_exps, con
  *   (TERN_ERR_SHAPE: the tokens of an expert stay in LDS).
  *   workspace: tern_moe_workspace bytes (TERN_ERR_SHAPE if fewer), 256-byte
  *       aligned, for this call alone until the stream has passed it.
- * Hidden values and all sums are fp32; Y is rounded once.  Any T; tokens are
+ * All sums are fp32, and Y is rounded once.  A hidden value times its weight
+ * w is fp32; where Y is TERN_F32 it enters the down product with all its bits,
+ * where Y has 16 bits rounded to 2^-16 of itself, so that Y carries an error of
+ * 2^-16 sum |w h Wd| beside its own rounding.  A 128-weight block's sum, before
+ * its scale, has to stay below half the fp32 range.  Any T; tokens are
  * taken 64 at a time, each time reading the experts that they take.  The
  * result of a token does not depend on the other tokens of its call beyond
  * the order in which fp32 sums are formed, and repeated calls agree bit for

@@ -8,10 +8,13 @@
 //   h[e] = silu(Wg[e] x) * (Wu[e] x),  y = sum over e in S of w[e] Wd[e] h[e]
 // with ternary Wg, Wu (the two halves of gate_up) and Wd.  The weights become
 // +-2 / 0 operands (tern_device.h) of the 16-bit matrix instructions, a
-// 128-weight block's fp32 sum is multiplied by its fp16 scale.  w h is handed
-// to the down product as two bf16 terms, hi = bf16(w h) and lo = bf16(w h - hi):
-// 16 significant bits, so that this product adds no rounding that a 16-bit
-// output would show.
+// 128-weight block's fp32 sum is multiplied by its fp16 scale.  v = w h, an
+// fp32, is handed to the down product as bf16 terms that sum up to it: t1 =
+// bf16(v), t2 = bf16(v - t1), t3 = v - t1 - t2.  An fp32 output takes all three,
+// which is v exactly.  A 16-bit output takes two, which is v to 2^-16, a 32nd of
+// the half step of fp16: half the slots for an error of sum |v Wd| 2^-16.  The
+// terms are those of v / 4, so that no term and no product with +-2 leaves the
+// fp32 range before v does.
 //
 // Launches.  Up to kMoeSmall tokens take two: the up kernel, whose workgroups
 // each route every token anew (a microsecond, against two for a launch of its
@@ -172,8 +175,8 @@ __device__ __forceinline__ int nth_bit(const uint32_t *bits, int words, int n) {
     return -1;
 }
 
-// 16-bit words of a pair's hidden values.
-__host__ __device__ constexpr int64_t hid_words(int64_t F) { return (F + 511) / 512 * 1024; }
+// 16-bit words of a pair's hidden values in so many terms.
+__host__ __device__ constexpr int64_t hid_words(int64_t F, int terms) { return (F + 511) / 512 * 512 * terms; }
 
 // What the kernels hand on in the workspace.
 struct Plan {
@@ -182,7 +185,7 @@ struct Plan {
     int *experts;        // [slots] the taken experts
     int *start;          // [slots + 1] where an expert's pairs start, start[i] = start[i + 1]: not taken
     int *pairs;          // [P] pairs by expert
-    uint16_t *hid;       // [P, steps of F, 2, 512] bf16: weight * hidden value, hi and lo terms
+    uint16_t *hid;       // [P, steps of F, 2 or 3 terms, 512] bf16: weight * hidden value / 4
     float *part;         // [P, H]
 };
 
@@ -248,8 +251,9 @@ __device__ __forceinline__ float4v_t mfma16(const uint4 &a, const uint4 &b, cons
                                                        0, 0, 0);
 }
 
-// AT: activations fp16 (0), bf16 (1) or fp32 (2: hi and lo terms in slots s and s + 2).
-constexpr int rows_per_set(int at) { return at == 2 ? 2 : 4; }
+// AT: activations fp16 (0), bf16 (1) or fp32 in that many bf16 terms (2, 3).  Term m of row j of a
+// set is in slot j + rows_per_set m; with three terms the fourth slot is empty.
+__host__ __device__ constexpr int rows_per_set(int at) { return at == 3 ? 1 : at == 2 ? 2 : 4; }
 
 // Rows of weights and scales: quads [0, Q / 2) in a, the others in b.
 struct Rows {
@@ -311,26 +315,27 @@ __device__ __forceinline__ void stage(char *ops, const char *x, const int64_t *o
     }
 }
 
-// Where the up kernel leaves hidden value f of a pair, in 16-bit words, the lo term 512 behind: a
-// step's operands in the order in which the down kernels take them, [operand][ca][p][8].
-__device__ __forceinline__ int hidden_at(int f) {
+// Where the up kernel leaves hidden value f of a pair, in 16-bit words, each term 512 behind the
+// one before: a step's operands in the order in which the down kernels take them, [operand][ca][p][8].
+__device__ __forceinline__ int hidden_at(int f, int terms) {
     const int k = f & 511, ca = k >> 7, p = (k >> 5) & 3, x = k & 15, j = x & 7;
     const int i = ((k >> 4) & 1) * 2 + (j >> 2);
-    return (f >> 9) * 1024 + ((i * 4 + ca) * 4 + p) * 8 + (j & 3) * 2 + (x >> 3);
+    return (f >> 9) * 512 * terms + ((i * 4 + ca) * 4 + p) * 8 + (j & 3) * 2 + (x >> 3);
 }
 
-// Hidden values of pairs rowpair[j] into LDS (-1: none): row j is slots j % 2 and j % 2 + 2 of set j / 2.
-template <int SETS>
+// Hidden values of pairs rowpair[j] into LDS (-1: none), row j in set j / rows_per_set.
+template <int AT, int SETS>
 __device__ __forceinline__ void stage_hidden(char *ops, const uint16_t *hid, const int *rowpair, int groups, int tid,
                                              int nthreads) {
-    const int steps = (groups + 3) / 4, per_row = steps * 128;   // chunks of 16 bytes
-    for (int i = tid; i < SETS * 2 * per_row; i += nthreads) {
+    constexpr int R = rows_per_set(AT), TERMS = 4 / R;   // with the empty one
+    const int steps = (groups + 3) / 4, per_row = steps * TERMS * 64;   // chunks of 16 bytes
+    for (int i = tid; i < SETS * R * per_row; i += nthreads) {
         const int j = i / per_row, k = i - j * per_row;
-        const int s = k >> 7, term = (k >> 6) & 1, op = (k >> 4) & 3, ca = (k >> 2) & 3, p = k & 3;
+        const int s = k / (TERMS * 64), term = (k >> 6) % TERMS, op = (k >> 4) & 3, ca = (k >> 2) & 3, p = k & 3;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (rowpair[j] >= 0 && 4 * s + ca < groups)
-            v = *reinterpret_cast<const uint4 *>(hid + ((int64_t)rowpair[j] * per_row + k) * 8);
-        *reinterpret_cast<uint4 *>(ops + ((s * SETS + j / 2) * 4 + op) * 1024 + (16 * p + 4 * ca + j % 2 + 2 * term) * 16) = v;
+        if (rowpair[j] >= 0 && 4 * s + ca < groups && term < AT)
+            v = *reinterpret_cast<const uint4 *>(hid + (((int64_t)rowpair[j] * steps + s) * AT + term) * 512 + (k & 63) * 8);
+        *reinterpret_cast<uint4 *>(ops + ((s * SETS + j / R) * 4 + op) * 1024 + (16 * p + 4 * ca + j % R + R * term) * 16) = v;
     }
 }
 
@@ -404,7 +409,17 @@ __device__ __forceinline__ void store_sums(float *sums, int lane, const float4v_
 template <int SETS>
 __device__ __forceinline__ float sum_of(const float *sums, int t, int q, int slot, int r) {
     const float4 v = *reinterpret_cast<const float4 *>(sums + (q * SETS + t) * 64 + slot * 16 + r * 4);
-    return 0.5f * ((v.x + v.y) + (v.z + v.w));   // the weights were +-2
+    return (v.x + v.y) + (v.z + v.w);
+}
+
+// The same over the terms of hidden row i, the smallest first.
+template <int AT, int SETS>
+__device__ __forceinline__ float sum_of_terms(const float *sums, int i, int q, int r) {
+    constexpr int R = rows_per_set(AT);
+    float y = sum_of<SETS>(sums, i / R, q, i % R + R * (AT - 1), r);
+#pragma unroll
+    for (int m = AT - 2; m >= 0; --m) y += sum_of<SETS>(sums, i / R, q, i % R + R * m, r);
+    return 2.f * y;   // the weights were +-2, the hidden values quarters
 }
 
 // Floats of a wave's sums.
@@ -494,7 +509,7 @@ template <int AT, int SETS, int Q, int G, bool SMALL>
 __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__restrict__ X, const void *__restrict__ logits,
                                                              int l_dtype, const uint8_t *__restrict__ GU,
                                                              const uint16_t *__restrict__ GUS, Plan plan, int T, int E,
-                                                             int top_k, int renorm, int H, int F) {
+                                                             int top_k, int renorm, int H, int F, int terms) {
     static_assert(Q % 2 == 0, "gate and up quads");
     constexpr int ROWS = SETS * rows_per_set(AT);
     static_assert(!SMALL || ROWS >= kMoeSmall, "a slot a token");
@@ -578,16 +593,19 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
 #pragma unroll
                 for (int o0 = 0; o0 < ROWS * 2 * Q; o0 += 64) {
                     const int o = o0 + lane, ff = o % (2 * Q), i = min(o / (2 * Q), ROWS - 1), f = u * 2 * Q + ff;
-                    const float g = sum_of<S>(sm, i / 4, ff / 4, i % 4, ff % 4);
-                    const float y = sum_of<S>(sm, i / 4, ff / 4 + Q / 2, i % 4, ff % 4);
+                    // the weights were +-2
+                    const float g = 0.5f * sum_of<S>(sm, i / 4, ff / 4, i % 4, ff % 4);
+                    const float y = 0.5f * sum_of<S>(sm, i / 4, ff / 4 + Q / 2, i % 4, ff % 4);
                     const int pr = rowpair[i];
-                    const float h = g / (1.f + expf(-g)) * y * rowweight[i];
-                    const __bf16 hi = (__bf16)h;
-                    const __bf16 lo = (__bf16)(__builtin_isinf((float)hi) ? 0.f : h - (float)hi);   // infinity has no rest
+                    const float h = 0.25f * (g / (1.f + expf(-g)) * y * rowweight[i]);
+                    const __bf16 t1 = (__bf16)h;
+                    const float h1 = __builtin_isinf(h) ? 0.f : h - (float)t1;   // infinity has no rest
+                    const __bf16 t2 = (__bf16)h1;
                     if (o < ROWS * 2 * Q && pr >= 0 && f < F) {
-                        uint16_t *at = plan.hid + (int64_t)pr * hid_words(F) + hidden_at(f);
-                        at[0] = __builtin_bit_cast(uint16_t, hi);
-                        at[512] = __builtin_bit_cast(uint16_t, lo);
+                        uint16_t *at = plan.hid + (int64_t)pr * hid_words(F, terms) + hidden_at(f, terms);
+                        at[0] = __builtin_bit_cast(uint16_t, t1);
+                        at[512] = __builtin_bit_cast(uint16_t, t2);
+                        if (terms == 3) at[1024] = __builtin_bit_cast(uint16_t, (__bf16)(h1 - (float)t2));
                     }
                 }
             });
@@ -600,10 +618,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
 }
 
 // part[pair][n] = (Wd h)[n], 4 Q values n a unit.
-template <int SETS, int Q, int G>
+template <int AT, int SETS, int Q, int G>
 __global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t *__restrict__ D,
                                                                const uint16_t *__restrict__ DS, Plan plan, int H, int F) {
-    constexpr int ROWS = SETS * rows_per_set(2);
     extern __shared__ float4 lds4[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -617,13 +634,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t 
     const int units = (H + 4 * Q - 1) / (4 * Q);
     int base = 0;
     auto go = [&](auto sets) __attribute__((always_inline)) {
-        constexpr int S = decltype(sets)::value, ROWS = S * rows_per_set(2);
-        product<2, S, Q, G>(
+        constexpr int S = decltype(sets)::value, ROWS = S * rows_per_set(AT);
+        product<AT, S, Q, G>(
             [&]() __attribute__((always_inline)) {
                 if (base > 0) __syncthreads();   // the operands of the chunk before are read
                 if (tid < ROWS) rowpair[tid] = base + tid < count ? plan.pairs[start + base + tid] : -1;
                 __syncthreads();
-                stage_hidden<S>(ops, plan.hid, rowpair, groups, tid, 64 * kWaves);
+                stage_hidden<AT, S>(ops, plan.hid, rowpair, groups, tid, 64 * kWaves);
                 __syncthreads();
             },
             ops, sums + wave * sums_floats<SETS, Q>(), blockIdx.x * kWaves + wave, gridDim.x * kWaves, units, groups, lane,
@@ -636,8 +653,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t 
 #pragma unroll
                 for (int o0 = 0; o0 < ROWS * 4 * Q; o0 += 64) {
                     const int o = o0 + lane, nn = o % (4 * Q), i = min(o / (4 * Q), ROWS - 1), n = u * 4 * Q + nn;
-                    const float y = sum_of<S>(sm, i / 2, nn / 4, i % 2, nn % 4) +
-                                    sum_of<S>(sm, i / 2, nn / 4, i % 2 + 2, nn % 4);
+                    const float y = sum_of_terms<AT, S>(sm, i, nn / 4, nn % 4);
                     const int pr = rowpair[i];
                     if (o < ROWS * 4 * Q && pr >= 0 && n < H) plan.part[(int64_t)pr * H + n] = y;
                 }
@@ -645,7 +661,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_down_kernel(const uint8_t 
         base += ROWS;
     };
     while (base < count) {
-        if (SETS > 1 && count - base <= rows_per_set(2)) go(std::integral_constant<int, 1>());
+        if (SETS > 1 && count - base <= rows_per_set(AT)) go(std::integral_constant<int, 1>());
         else go(std::integral_constant<int, SETS>());
     }
 }
@@ -680,12 +696,13 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(Plan plan, void *__restric
 // Few tokens: a workgroup goes through every taken expert for its rows of Y.  Its waves take the
 // (expert, step) units in turn; the slots of the tiles are the tokens.  One that did not take the
 // expert at hand has zeros there, and zeros in place of the expert's scales: they need not be finite.
-template <int SETS, int Q>
+template <int AT, int SETS, int Q>
 __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__restrict__ D,
                                                             const uint16_t *__restrict__ DS, Plan plan,
                                                             void *__restrict__ Y, int y_dtype, int T, int E, int top_k,
                                                             int H, int F, int nw) {
-    static_assert(SETS * rows_per_set(2) <= kMoeSmall, "tokens");
+    constexpr int R = rows_per_set(AT);
+    static_assert(SETS * R <= kMoeSmall, "tokens");
     extern __shared__ float4 lds4[];
     float *red = reinterpret_cast<float *>(lds4);
     int *ids = reinterpret_cast<int *>(red + nw * sums_floats<SETS, Q>());
@@ -723,9 +740,9 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
     __syncthreads();
     const int taken = uniform(experts[kMoeSmall * kMoeMaxTopK]);
     const int groups = F >> 7, n0 = blockIdx.x * 4 * Q, steps = (groups + 3) / 4, units = taken * steps;
-    const int ca = (lane & 15) >> 2, slot = lane & 3, per_pair = (int)hid_words(F) * 2;
+    const int ca = (lane & 15) >> 2, slot = lane & 3, per_pair = (int)hid_words(F, AT) * 2;
     const __amdgpu_buffer_rsrc_t rx = buffer_of(plan.hid, P * per_pair);
-    const int lane_at = (slot >> 1) * 1024 + (ca * 4 + (lane >> 4)) * 16;   // in a step's 2 KB
+    const int lane_at = slot / R * 1024 + (ca * 4 + (lane >> 4)) * 16;   // in a step's terms, 1 KB each
 
     uint4 a[SETS][4];
     uint64_t took[SETS];   // bit of a slot's lane: its token took the unit's expert
@@ -738,9 +755,9 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
         const int i = live ? u / steps : 0, s = live ? u - i * steps : 0, e = uniform(experts[i]);
 #pragma unroll
         for (int t = 0; t < SETS; ++t) {
-            const int tok = 2 * t + (slot & 1), pr = live && tok < T ? pair[i * T + min(tok, T - 1)] : -1;
+            const int tok = R * t + slot % R, pr = live && slot / R < AT && tok < T ? pair[i * T + min(tok, T - 1)] : -1;
             took[t] = __ballot(pr >= 0);
-            const int off = pr >= 0 && 4 * s + ca < groups ? pr * per_pair + s * 2048 + lane_at : OUT_OF_RANGE;
+            const int off = pr >= 0 && 4 * s + ca < groups ? pr * per_pair + s * (AT * 1024) + lane_at : OUT_OF_RANGE;
 #pragma unroll
             for (int k = 0; k < 4; ++k) a[t][k] = load16(rx, off + k * 256);
         }
@@ -767,7 +784,7 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
             fetch(u + nw);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                quad<2, SETS>(st.code[q], st.scale[q], now, acc[q], [&](int t, int i) { return (takers[t] >> i & 1) != 0; });
+                quad<AT, SETS>(st.code[q], st.scale[q], now, acc[q], [&](int t, int i) { return (takers[t] >> i & 1) != 0; });
                 load_quad<Q>(st, w, at, groups, q);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -782,7 +799,7 @@ __global__ __launch_bounds__(512) void moe_down_small_kernel(const uint8_t *__re
         float y = 0.f;
         for (int w = tid & 3; w < nw; w += 4) {
             const float *sm = red + w * sums_floats<SETS, Q>();
-            y += sum_of<SETS>(sm, i / 2, nn / 4, i % 2, nn % 4) + sum_of<SETS>(sm, i / 2, nn / 4, i % 2 + 2, nn % 4);
+            y += sum_of_terms<AT, SETS>(sm, i, nn / 4, nn % 4);
         }
         y += __builtin_bit_cast(float, dpp<0xB1>(__builtin_bit_cast(uint32_t, y)));
         y += __builtin_bit_cast(float, dpp<0x4E>(__builtin_bit_cast(uint32_t, y)));
@@ -811,7 +828,7 @@ Plan plan_of(void *ws, int64_t P, int64_t H, int64_t F) {
     p.experts = reinterpret_cast<int *>(take((size_t)P * 4));
     p.start = reinterpret_cast<int *>(take((size_t)(P + 1) * 4));
     p.pairs = reinterpret_cast<int *>(take((size_t)P * 4));
-    p.hid = reinterpret_cast<uint16_t *>(take((size_t)P * hid_words(F) * 2));
+    p.hid = reinterpret_cast<uint16_t *>(take((size_t)P * hid_words(F, 3) * 2));
     p.part = reinterpret_cast<float *>(w);
     return p;
 }
@@ -825,6 +842,8 @@ int workgroups(int64_t units, int slots) {
 
 constexpr size_t kLds = 160 * 1024;
 
+int hidden_terms(const MoeArgs &a) { return a.y_dtype == 2 ? 3 : 2; }
+
 template <int AT, int SETS, int Q, int G, bool SMALL>
 hipError_t launch_up(const MoeArgs &a, const Plan &plan, int slots) {
     const size_t lds = ops_bytes<SETS>((int)(a.H / 128)) + kWaves * sums_floats<SETS, Q>() * 4 +
@@ -836,31 +855,31 @@ hipError_t launch_up(const MoeArgs &a, const Plan &plan, int slots) {
     const hipError_t e = raise_lds_limit<kern>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, g, b, lds, a.stream, static_cast<const char *>(a.X), a.logits, a.l_dtype, a.GU, a.GUS, plan,
-                       (int)a.T, (int)a.E, (int)a.top_k, a.renormalize, (int)a.H, (int)a.F);
+                       (int)a.T, (int)a.E, (int)a.top_k, a.renormalize, (int)a.H, (int)a.F, hidden_terms(a));
     return hipGetLastError();
 }
 
-template <int SETS, int Q, int G>
+template <int AT, int SETS, int Q, int G>
 hipError_t launch_down(const MoeArgs &a, const Plan &plan, int slots) {
-    const size_t lds = ops_bytes<SETS>((int)(a.F / 128)) + kWaves * sums_floats<SETS, Q>() * 4 + SETS * rows_per_set(2) * 4;
+    const size_t lds = ops_bytes<SETS>((int)(a.F / 128)) + kWaves * sums_floats<SETS, Q>() * 4 + SETS * rows_per_set(AT) * 4;
     if constexpr (SETS > 1)
-        if (lds > kLds) return launch_down<SETS / 2, Q, G>(a, plan, slots);
+        if (lds > kLds) return launch_down<AT, SETS / 2, Q, G>(a, plan, slots);
     const dim3 g((unsigned)workgroups((a.H + 4 * Q - 1) / (4 * Q), slots), (unsigned)slots), b(64 * kWaves);
-    constexpr auto kern = &moe_down_kernel<SETS, Q, G>;
+    constexpr auto kern = &moe_down_kernel<AT, SETS, Q, G>;
     const hipError_t e = raise_lds_limit<kern>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, g, b, lds, a.stream, a.D, a.DS, plan, (int)a.H, (int)a.F);
     return hipGetLastError();
 }
 
-template <int SETS, int Q>
+template <int AT, int SETS, int Q>
 hipError_t launch_down_small(const MoeArgs &a, const Plan &plan) {
     const int64_t units = a.T * a.top_k * ((a.F + 511) / 512);   // at most
     const int nw = (int)(units < 8 ? units : 8);
     const dim3 g((unsigned)((a.H + 4 * Q - 1) / (4 * Q))), b(64 * nw);
     const size_t lds = (size_t)nw * sums_floats<SETS, Q>() * 4 + kMoeSmall * kMoeMaxTopK * 4 * (2 + kMoeSmall) +
                        kMoeMaxExperts / 8 + 4;
-    constexpr auto kern = &moe_down_small_kernel<SETS, Q>;
+    constexpr auto kern = &moe_down_small_kernel<AT, SETS, Q>;
     const hipError_t e = raise_lds_limit<kern>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, g, b, lds, a.stream, a.D, a.DS, plan, a.Y, a.y_dtype, (int)a.T, (int)a.E, (int)a.top_k,
@@ -870,20 +889,21 @@ hipError_t launch_down_small(const MoeArgs &a, const Plan &plan) {
 
 // Rows of a workgroup of the small down kernel: one workgroup a CU where they allow it, else few
 // rounds of them (four tokens, H = 5120: 16, 24, 32 rows 13.9, 9.4, 10.9 us; H = 2048: 16 rows 2 us
-// more than 8).
-template <int SETS>
+// more than 8).  Four sets leave registers for 16 rows.
+template <int AT, int SETS>
 hipError_t down_small(const MoeArgs &a, const Plan &plan) {
+    constexpr int MOST = SETS > 2 ? 4 : 8;
     int best = 0, least = 0;
-    for (int q = 2; q <= 8; q += 2) {
+    for (int q = 2; q <= MOST; q += 2) {
         const int cost = (int)(((a.H + 4 * q - 1) / (4 * q) + 255) / 256) * (q + 1);
         if (best == 0 || cost < least) least = cost, best = q;
     }
-    switch (best) {
-    case 2: return launch_down_small<SETS, 2>(a, plan);
-    case 4: return launch_down_small<SETS, 4>(a, plan);
-    case 6: return launch_down_small<SETS, 6>(a, plan);
-    default: return launch_down_small<SETS, 8>(a, plan);
+    if (best == 2) return launch_down_small<AT, SETS, 2>(a, plan);
+    if constexpr (MOST > 4) {
+        if (best == 6) return launch_down_small<AT, SETS, 6>(a, plan);
+        if (best == 8) return launch_down_small<AT, SETS, 8>(a, plan);
     }
+    return launch_down_small<AT, SETS, 4>(a, plan);
 }
 
 // Steps of K that come in twos rather than in fours.  The up kernel takes them so, with twice the rows
@@ -898,6 +918,7 @@ hipError_t up(const MoeArgs &a, const Plan &plan, int slots) {
     return a.x_dtype == 0 ? launch_up<0, SETS, 2, 4, SMALL>(a, plan, slots) : launch_up<1, SETS, 2, 4, SMALL>(a, plan, slots);
 }
 
+template <int AT>
 hipError_t launch_chunk(const MoeArgs &a) {
     const int P = (int)(a.T * a.top_k);
     const Plan plan = plan_of(a.ws, P, a.H, a.F);
@@ -906,7 +927,11 @@ hipError_t launch_chunk(const MoeArgs &a) {
     if (a.T <= kMoeSmall) {
         e = up<1, true>(a, plan, slots);
         if (e != hipSuccess) return e;
-        return a.T <= 2 ? down_small<1>(a, plan) : down_small<2>(a, plan);
+        constexpr int R = rows_per_set(AT);
+        if (a.T <= R) return down_small<AT, 1>(a, plan);
+        if constexpr (2 * R < kMoeSmall)
+            if (a.T > 2 * R) return down_small<AT, 4>(a, plan);
+        return down_small<AT, 2>(a, plan);
     }
     hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.logits, a.l_dtype, (int)a.T, (int)a.E,
                        (int)a.top_k, a.renormalize, slots, plan);
@@ -915,7 +940,7 @@ hipError_t launch_chunk(const MoeArgs &a) {
     // A second set of slots once the experts have more than two tokens in the mean.
     e = P > 2 * slots ? up<2, false>(a, plan, slots) : up<1, false>(a, plan, slots);
     if (e != hipSuccess) return e;
-    e = few_steps(a.F) ? launch_down<2, 4, 2>(a, plan, slots) : launch_down<2, 2, 4>(a, plan, slots);
+    e = few_steps(a.F) ? launch_down<AT, 2, 4, 2>(a, plan, slots) : launch_down<AT, 2, 2, 4>(a, plan, slots);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256), 0, a.stream, plan,
                        a.Y, a.y_dtype, (int)a.top_k, (int)a.H);
@@ -926,7 +951,7 @@ hipError_t launch_chunk(const MoeArgs &a) {
 
 size_t moe_workspace(int64_t T, int64_t top_k, int64_t H, int64_t F) {
     const int64_t P = (T < kMoeChunk ? T : kMoeChunk) * top_k;
-    return 4 * align256((size_t)P * 4) + align256((size_t)(P + 1) * 4) + align256((size_t)P * hid_words(F) * 2) +
+    return 4 * align256((size_t)P * 4) + align256((size_t)(P + 1) * 4) + align256((size_t)P * hid_words(F, 3) * 2) +
            align256((size_t)P * H * 4);
 }
 
@@ -938,7 +963,7 @@ hipError_t launch_moe(const MoeArgs &a0) {
         a.X = static_cast<const char *>(a0.X) + t * a.H * 2;
         a.logits = static_cast<const char *>(a0.logits) + t * a.E * lsize;
         a.Y = static_cast<char *>(a0.Y) + t * a.H * ysize;
-        const hipError_t e = launch_chunk(a);
+        const hipError_t e = hidden_terms(a) == 3 ? launch_chunk<3>(a) : launch_chunk<2>(a);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
