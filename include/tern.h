@@ -247,9 +247,10 @@ tern_status tern_mx_dequant(const uint8_t *codes, const uint8_t *exps, void *W, 
  * X in TERN_F16 or TERN_BF16, sums in fp32, Y in any of the three types,
  * rounded once (nearest even).  Any M, K <= 2^24.  X 16-byte aligned, Y to its
  * element.
- * The products are exact.  An infinity or NaN in a row of X reaches that row
- * of Y only, one in a row of W (a block with exponent 255, or values beyond
- * the fp32 range) that column only.
+ * The products are exact.  An infinity in X gives infinities, or NaN where its
+ * weight is zero; a NaN gives NaN.  Either reaches its row of Y only, one in a
+ * row of W (a block with exponent 255, or values beyond the fp32 range) that
+ * column only.
  */
 tern_status tern_mx_matmul(const void *X, tern_dtype x_dtype, const uint8_t *codes, const uint8_t *exps, void *Y,
                            tern_dtype y_dtype, int64_t M, int64_t N, int64_t K, hipStream_t stream);

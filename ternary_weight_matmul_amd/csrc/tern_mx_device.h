@@ -18,11 +18,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// The two bf16 terms of 8 fp16 values, hi (returned) and lo.  hi is the value
-// without its last 3 significant bits, lo those bits: hi + lo is the value
-// exactly.  (An infinity has the lo inf - inf, NaN.)
+// The two bf16 terms of 8 fp16 values, hi (returned) and lo.  lo is the last 3 significant bits of
+// the value, hi the rest: hi + lo is the value exactly.  An infinity leaves inf - inf behind, which
+// the maximum replaces by a number (it returns the operand that is one): the infinity is in hi
+// alone.  A NaN makes hi a NaN.
 __device__ __forceinline__ uint4 fp16_terms(const uint4 &q, uint4 &lo) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const half2_t least = {(_Float16)-65504.f, (_Float16)-65504.f};
     uint32_t h[4], l[4];
     // the upper halves of two fp32: exact, both terms have 8 significant bits at most
     auto pair = [](half2_t v) {
@@ -32,8 +34,9 @@ __device__ __forceinline__ uint4 fp16_terms(const uint4 &q, uint4 &lo) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const half2_t v = __builtin_bit_cast(half2_t, w[i]), t = __builtin_bit_cast(half2_t, w[i] & 0xFFF8FFF8u);
-        h[i] = pair(t);
-        l[i] = pair(v - t);
+        const half2_t d = __builtin_elementwise_max(v - t, least);
+        h[i] = pair(v - d);
+        l[i] = pair(d);
     }
     lo = make_uint4(l[0], l[1], l[2], l[3]);
     return make_uint4(h[0], h[1], h[2], h[3]);
