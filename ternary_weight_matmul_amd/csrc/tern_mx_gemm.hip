@@ -406,8 +406,10 @@ hipError_t launch_t(const MxArgs &a) {
 // holds one big tile at a time; up to 256 small ones take as long as one.  Measured, K = 5120, us:
 //   16-bit X: 512 -> 5120: big 120, small 59; 256 -> 17408: 124, 104; 1024 -> 5120: 122, 95;
 //   512 -> 17408: 133, 162.  4-bit X: 44, 28; 48, 45; 43, 36; 50, 64.
+// A launch has fewer than 2^32 threads: 2^24 small tiles are too many.
 template <int XT>
 bool big_tiles(const MxArgs &a) {
+    if (((a.M + 63) / 64) * ((a.N + 127) / 128) >= (1 << 24)) return true;
     const double big = (double)((a.M + 255) / 256) * (double)((a.N + (XT == 2 ? 191 : 255)) / (XT == 2 ? 192 : 256)) / 256;
     const double small = (double)((a.M + 63) / 64) * (double)((a.N + 127) / 128) / 256;
     const double step = XT == 2 ? 2.6 : 2.4 + (big < 1 ? big : 1);
@@ -426,12 +428,13 @@ hipError_t launch_x(const MxArgs &a) {
 // small, too few tiles to fill the chip take longer than the weights read once for 16 rows.  Measured,
 // K = 5120, us, in sixteens and in tiles: 16-bit X, 128 -> 5120 40 and 45, 64 -> 17408 59 and 49;
 // 4-bit X, 64 -> 5120 18 and 25, 128 -> 5120 27 and 23; 37 x 1056 -> 1001: 4 and 13.
-// Scale bytes are loaded 16 at a time, offsets inside a tile are 32-bit, tiles are counted in an int.
+// Scale bytes are loaded 16 at a time, offsets inside a tile are 32-bit, and so are the columns that a
+// tile would have past the last one.  2^23 big tiles are too many threads for a launch.
 bool mx_gemm_wins(const MxArgs &a) {
     const int64_t blocks = a.K / 32, chunks = (a.M + 15) / 16;
     if (a.M <= 32 || (chunks <= 10 && chunks * a.N <= (a.x_dtype == 2 ? 32768 : 45056))) return false;
-    return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) &&
-           ((a.M + 63) / 64) * ((a.N + 63) / 64) < (int64_t(1) << 31);
+    return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) && a.N < INT32_MAX - 256 &&
+           ((a.M + 255) / 256) * ((a.N + 191) / 192) < (1 << 23);
 }
 
 hipError_t launch_mx_gemm(const MxArgs &a) {
