@@ -85,3 +85,71 @@ def test_most_rows_and_columns(M, N, kind):
     for at in range(0, flat.numel(), step):
         other += int((flat[at:at + step] != 16).sum())
     assert other == M * N - (M - len(rows)) * (N - len(cols))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 24, 288), (2, 72, 1056), (4, 100, 512), (8, 40, 1184), (16, 130, 544),
+                                   (24, 33, 320), (70, 300, 288), (200, 130, 1056), (700, 9300, 96)])
+def test_every_bit_of_fp16_activations(M, N, K):
+    """Integers of 11 significant bits in every place, against multiples of a half: all sums are
+    exact, so an activation's last bits are seen wherever they are lost or misplaced."""
+    rng = np.random.default_rng(M + N)
+    x = rng.integers(1025, 2048, (M, K)) * rng.choice([-1.0, 1.0], (M, K))
+    x[rng.random((M, K)) < 0.5] *= 0.5   # two exponents side by side, sums are multiples of a quarter
+    codes = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    exps = np.full((N, K // 32), 127, dtype=np.uint8)
+    W = R.values(codes, exps)
+    assert (np.abs(x) @ np.abs(W).T).max() * 4 < 2 ** 24
+    want = x @ W.T
+    xt = torch.from_numpy(x).half()
+    assert np.array_equal(R.f64(xt), x)
+    y = tern.mx_matmul_into(xt.to(DEV), dev(codes), dev(exps), nan_out(M, N, "f32"))
+    assert np.array_equal(R.f64(y), want)
+
+
+@pytest.mark.parametrize("M", [1, 4, 9, 255])
+def test_every_pair_of_scales_of_4_bit_operands(M):
+    """One value in a block of zeros: the product's scale is the sum of two exponent bytes, over all
+    255 x 255 of them, subnormal results and infinities included."""
+    K, k, rows = 96, 40, torch.arange(255, dtype=torch.uint8)
+    wc = torch.full((255, K // 2), 0x22, dtype=torch.uint8)   # ones
+    we = rows[:, None].repeat(1, K // 32)
+    for a in range(0, 255, M):
+        xe = rows[a:a + M, None].repeat(1, K // 32)
+        xc = torch.zeros((xe.shape[0], K // 2), dtype=torch.uint8)
+        xc[:, k // 2] = 2
+        y = tern.mx_matmul_mx(xc.to(DEV), xe.to(DEV), wc.to(DEV), we.to(DEV), out_dtype=torch.float32).cpu()
+        want = torch.pow(2.0, (xe[:, :1].double() - 127) + (rows[None].double() - 127)).float()
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 1056), (6, 130, 288), (16, 64, 512), (70, 300, 288), (300, 600, 544)])
+def test_4_bit_operands_with_scales_far_apart(M, N, K):
+    """Blocks whose scales differ by up to 2^60, zero blocks (exponent 0) among them: within the bound
+    of fp32 sums of exact products."""
+    rng = np.random.default_rng(K)
+    xc, wc = (rng.integers(0, 256, (r, K // 2)).astype(np.uint8) for r in (M, N))
+    xe, we = (rng.integers(97, 158, (r, K // 32)).astype(np.uint8) for r in (M, N))
+    zero = rng.random((M, K // 32)) < 0.2
+    zero[:, 0] = True
+    xe[zero] = 0
+    xc.reshape(M, K // 32, 16)[zero] = 0
+    X, W = R.values(xc, xe), R.values(wc, we)
+    want = X @ W.T
+    y = tern.mx_matmul_mx_into(dev(xc), dev(xe), dev(wc), dev(we), nan_out(M, N, "f32"))
+    R.assert_close(y, want, R.product_bound(X, W, want, torch.float32))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 255, 64), (5, 255, 1056), (70, 255, 288), (300, 600, 544)])
+@pytest.mark.parametrize("xd", ["f16", "bf16"])
+@pytest.mark.parametrize("v", [1.0, 2.0 ** -14, 3 * 2.0 ** 12])
+def test_every_scale_against_16_bit_activations(M, N, K, xd, v):
+    """Single weights of a half read back through every exponent byte but 255, subnormal bf16 weights
+    and subnormal results included."""
+    exps = np.repeat((np.arange(N) % 255).astype(np.uint8)[:, None], K // 32, axis=1)
+    codes = np.full((N, K // 2), 0x11, dtype=np.uint8)
+    x = torch.zeros((M, K))
+    x[torch.arange(M), (torch.arange(M) * 37 + 5) % K] = v
+    y = tern.mx_matmul_into(x.to(DT[xd]).to(DEV), dev(codes), dev(exps), nan_out(M, N, "f32")).cpu()
+    with np.errstate(over="ignore"):
+        want = (0.5 * v * np.exp2(exps[:, 0].astype(np.float64) - 127)).astype(np.float32)
+    assert np.array_equal(y.numpy(), np.broadcast_to(want, (M, N)))
