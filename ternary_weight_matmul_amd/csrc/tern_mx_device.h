@@ -27,16 +27,17 @@ __device__ __forceinline__ uint4 fp16_terms(const uint4 &q, uint4 &lo) {
     const half2_t least = {(_Float16)-65504.f, (_Float16)-65504.f};
     uint32_t h[4], l[4];
     // the upper halves of two fp32: exact, both terms have 8 significant bits at most
-    auto pair = [](half2_t v) {
-        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, (float)v[1]), __builtin_bit_cast(uint32_t, (float)v[0]),
-                                     0x07060302u);
+    auto pair = [](float a, float b) {
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
     };
+    float one = 1.f;   // hidden, for a multiply-add that takes 16-bit operands: no conversion of v - d
+    asm("" : "+s"(one));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const half2_t v = __builtin_bit_cast(half2_t, w[i]), t = __builtin_bit_cast(half2_t, w[i] & 0xFFF8FFF8u);
         const half2_t d = __builtin_elementwise_max(v - t, least);
-        h[i] = pair(v - d);
-        l[i] = pair(d);
+        h[i] = pair(fmaf((float)v[0], one, -(float)d[0]), fmaf((float)v[1], one, -(float)d[1]));
+        l[i] = pair((float)d[0], (float)d[1]);
     }
     lo = make_uint4(l[0], l[1], l[2], l[3]);
     return make_uint4(h[0], h[1], h[2], h[3]);
