@@ -12,7 +12,9 @@
 // fp32, is handed to the down product as bf16 terms that sum up to it: t1 =
 // bf16(v), t2 = bf16(v - t1), t3 = v - t1 - t2.  An fp32 output takes all three,
 // which is v exactly.  A 16-bit output takes two, which is v to 2^-16, a 32nd of
-// the half step of fp16: half the slots for an error of sum |v Wd| 2^-16.  The
+// the half step of fp16: an error of sum |v Wd| 2^-16, for half the slots (an
+// fp32 output instead of a 16-bit one: 1 token 12.9 us either way, 32 tokens of
+// the sizes below 68 -> 85, 4 tokens of 8 experts of 5120 x 2048 25 -> 41).  The
 // terms are those of v / 4, so that no term and no product with +-2 leaves the
 // fp32 range before v does.
 //
@@ -37,9 +39,9 @@
 // below, against 58.
 //
 // Bound: latency for one token (E = 64, k = 8, 2048 x 1024: 12.6 MB of codes,
-// 3.7 us for a plain read; up 8.1 us, routing first, and down 5.8).  At 32
+// 3.7 us for a plain read; up 8.4 us, routing first, and down 5.4).  At 32
 // tokens (97 MB, 16 us) decoding the codes, 36 vector instructions a quad and
-// step, and the 4 or 8 matrix instructions they feed: 30 + 28 us, and 7 + 5
+// step, and the 4 or 8 matrix instructions they feed: 29 + 28 us, and 7 + 5
 // for the plan and the sum.
 #include <hip/hip_runtime.h>
 
@@ -504,7 +506,7 @@ static_assert(kWaves > kMoeSmall, "waves that fetch while others route");
 
 // hid[pair][f] = silu(g) * u, 2 Q values f a unit: quads [0, Q / 2) are gate rows, the rest the up
 // rows of the same f.  SMALL: routes by itself while other waves fetch the tokens, the slots are the
-// tokens, and the first workgroup leaves ids and weights behind for the down kernel.
+// tokens, and the first workgroup leaves the ids behind for the down kernel.
 template <int AT, int SETS, int Q, int G, bool SMALL>
 __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__restrict__ X, const void *__restrict__ logits,
                                                              int l_dtype, const uint8_t *__restrict__ GU,

@@ -1,6 +1,6 @@
 // tern_mx.h -- host-side launchers and device helpers of the microscaled 4-bit
 // float (e2m1, one power-of-two scale per 32) operators.  Every launcher
-// assumes its arguments were validated by tern_mx_api.hip.
+// assumes its arguments were validated by tern_api.hip.
 //
 // Format.  A row of K values is cut into blocks of 32; block b has a biased
 // exponent byte e (the scale is 2^(e - 127), 255 means that the block is NaN)

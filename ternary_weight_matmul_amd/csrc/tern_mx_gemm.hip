@@ -26,7 +26,9 @@
 // LDS rows are XOR-swizzled in 16-byte chunks so that the lanes of a fragment
 // read that are served together fall on distinct banks.
 //
-// Bound: the matrix cores.
+// Bound: the matrix cores.  M = 2048, 5120 -> 7168, weights rotated over 2 GB:
+// bf16 X 146 us, 4-bit X 74, fp16 X 320 (twice the matrix instructions, and
+// every wave splits its fragments of X anew).
 #include <hip/hip_runtime.h>
 
 #include <cmath>

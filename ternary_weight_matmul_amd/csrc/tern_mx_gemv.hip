@@ -33,8 +33,10 @@
 // took 12.7 to 16.9 us at M = 1 / 4, 5120 -> 17408 where this takes 12.9 /
 // 13.6, two steps of loads in flight or 12 waves 0.5 to 1 us more.
 //
-// Bound: HBM (the code bytes).  M = 1, 5120 -> 5120: 6.0 us (a plain read of
-// the bytes 3.7); M = 4, 5120 -> 17408: 13.6 (8.6); M = 16: 18.4.
+// Bound: HBM (the code bytes) and, from 16 rows, vector work.  Weights rotated
+// over 2 GB: M = 1, 5120 -> 5120 5.8 us (a plain read of the bytes 3.7); 5120 ->
+// 17408 (8.6) M = 4 13.6, M = 16 17.4, with fp16 X 15.0 and 21.5, 4-bit X 12.6
+// and 14.0.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
