@@ -430,11 +430,17 @@ hipError_t launch_x(const MxArgs &a) {
 // small, too few tiles to fill the chip take longer than the weights read once for 16 rows.  Measured,
 // K = 5120, us, in sixteens and in tiles: 16-bit X, 128 -> 5120 40 and 45, 64 -> 17408 59 and 49;
 // 4-bit X, 64 -> 5120 18 and 25, 128 -> 5120 27 and 23; 37 x 1056 -> 1001: 4 and 13.
+// More rows by a narrow W are as few tiles (a router over a prompt).  The border is a product of rows in
+// sixteens and N again.  Measured, us: 16-bit X, 200 x 5120 -> 64 5 and 37, 2048 x 1056 -> 128 11.6 and
+// 11.1, 1024 x 5120 -> 256 24 and 39, 512 x 5120 -> 1024 42 and 41, 1024 x 17408 -> 16 13 and 118; 4-bit
+// X, 200 x 5120 -> 64 5 and 15, 512 x 5120 -> 256 12 and 17, 161 x 1056 -> 1024 5.3 and 6.1, 1024 x 5120
+// -> 256 23 and 17.
 // Scale bytes are loaded 16 at a time, offsets inside a tile are 32-bit, and so are the columns that a
 // tile would have past the last one.  2^23 big tiles are too many threads for a launch.
 bool mx_gemm_wins(const MxArgs &a) {
     const int64_t blocks = a.K / 32, chunks = (a.M + 15) / 16;
-    if (a.M <= 32 || (chunks <= 10 && chunks * a.N <= (a.x_dtype == 2 ? 32768 : 45056))) return false;
+    const bool mx = a.x_dtype == 2;
+    if (a.M <= 32 || chunks * a.N <= (chunks <= 10 ? (mx ? 32768 : 45056) : (mx ? 11264 : 16384))) return false;
     return a.M * blocks >= 16 && a.N * blocks >= 16 && a.K <= (1 << 21) && a.N < INT32_MAX - 256 &&
            ((a.M + 255) / 256) * ((a.N + 191) / 192) < (1 << 23);
 }

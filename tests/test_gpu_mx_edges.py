@@ -153,3 +153,23 @@ def test_every_scale_against_16_bit_activations(M, N, K, xd, v):
     with np.errstate(over="ignore"):
         want = (0.5 * v * np.exp2(exps[:, 0].astype(np.float64) - 127)).astype(np.float32)
     assert np.array_equal(y.numpy(), np.broadcast_to(want, (M, N)))
+
+
+@pytest.mark.parametrize("M,N,K", [(200, 64, 5120), (1024, 16, 17408), (161, 1, 96), (2048, 8, 1056), (176, 1024, 288),
+                                   (177, 1489, 160), (513, 496, 544)])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "mx"])
+def test_many_rows_by_a_narrow_matrix(M, N, K, kind):
+    """The products of a router over a prompt, on either side of the border between the kernels."""
+    print(f"{M}x{K}->{N} {kind}", flush=True)
+    codes, exps = weights(N, K, M + N)
+    if kind == "mx":
+        xc, xe = weights(M, K, M * 3 + N, spread=4)
+        X = R.values(xc, xe)
+        y = tern.mx_matmul_mx_into(dev(xc), dev(xe), dev(codes), dev(exps), nan_out(M, N, "f32"))
+    else:
+        x = activations(M, K, kind, M)
+        X = R.f64(x)
+        y = tern.mx_matmul_into(x.to(DEV), dev(codes), dev(exps), nan_out(M, N, "f32"))
+    W = R.values(codes, exps)
+    want = X @ W.T
+    R.assert_close(y, want, R.product_bound(X, W, want, torch.float32))
