@@ -372,7 +372,8 @@ def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_
 def moe(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
         down: torch.Tensor, down_scales: torch.Tensor, top_k: int, renormalize: bool = True,
         out_dtype: Optional[torch.dtype] = None, group: int = 128) -> torch.Tensor:
-    """The layer's outputs [T,H] (of x's type unless out_dtype is given) as a new tensor."""
+    """The layer's outputs [T,H] (of x's type unless out_dtype is given) as a new tensor.  With fp32
+    outputs the hidden values keep all their bits, with 16-bit outputs 16 of them in less time."""
     out = x.new_empty(x.shape, dtype=out_dtype)
     return moe_into(x, logits, gate_up, gate_up_scales, down, down_scales, out, top_k, renormalize, group)
 

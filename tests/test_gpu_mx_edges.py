@@ -39,16 +39,22 @@ def test_infinities_and_nan_follow_the_sum(M, N, K, xd, bits):
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.fixture
+def free_memory():
+    """Nothing cached before a test that takes most of the memory, nor left behind it."""
+    torch.cuda.empty_cache()
+    yield torch.cuda.mem_get_info()[0]
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("M,N,kind", [(2 ** 31 - 1, 1, "mx"), (2 ** 31 - 300, 2, "mx"), (33, 2 ** 31 - 1, "bf16"),
                                       (60, 2 ** 30 - 4, "bf16")])
-def test_most_rows_and_columns(M, N, kind):
+def test_most_rows_and_columns(M, N, kind, free_memory):
     """Sizes whose tiles would be too many threads for a launch, or have columns past 2^31; the sums
     are exact, and the rows and columns that differ are the last ones and some in between."""
     K = 32
     need = (M + N) * 17 * (4 if kind == "bf16" and M > N else 1) + 2 * M * N + (8 << 30)
-    torch.cuda.empty_cache()
-    free, _ = torch.cuda.mem_get_info()
-    if free < need:
+    if free_memory < need:
         pytest.skip(f"needs {need >> 30} GB")
     print(f"{M}x{K}->{N} {kind}, {need >> 30} GB", flush=True)
     codes = torch.full((N, K // 2), 0x22, dtype=torch.uint8, device=DEV)   # ones
