@@ -15,7 +15,7 @@
  * Conventions shared by every entry point:
  *   - Every pointer is a DEVICE pointer the caller allocated and owns.  The
  *     library allocates no device memory, uses no scratch buffer but the
- *     workspace that a caller hands to tern_moe, and never frees or retains a
+ *     workspace that a caller hands to it, and never frees or retains a
  *     caller buffer.  Its only state across calls is a
  *     per-process record, per device and kernel instantiation, that the
  *     kernel's dynamic-LDS limit has been raised (hipFuncSetAttribute, done
@@ -297,6 +297,99 @@ tern_status tern_moe(const void *X, tern_dtype x_dtype, const void *logits, tern
                      const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E, int64_t top_k,
                      int64_t H, int64_t F, int32_t group, int32_t renormalize, void *workspace,
                      size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * 8-bit activations.  A matrix [M,K] is held as
+ *   codes [M,K] int8 and scales fp32, one per row ([M], q_group 0) or one per 128
+ *   consecutive values of a row ([M,K/128], q_group 128, which must divide K:
+ *   TERN_ERR_GROUP otherwise; any other q_group is TERN_ERR_UNSUPPORTED);
+ *   the value is code * scale.
+ * What is made here has a scale a / 127 for a row or block whose largest
+ * magnitude is a, and codes 127 v / a rounded to nearest, ties to even: in
+ * [-127, 127], and always the same for the same values.  A block of zeros has
+ * the scale 0.  One with an infinity or a NaN has the scale NaN and codes 0.
+ */
+
+/*
+ * tern_rms_norm -- root-mean-square norm of the rows of X[M,K], with the
+ * addition to a residual stream before it:
+ *   h = X + residual, rounded to the stream's type and written to residual_out
+ *       (without a residual h = X)
+ *   Y = h / sqrt(mean of h^2 over the row + eps) * weight, rounded once
+ *   codes, scales: the same values as 8-bit activations.  The largest |h weight|
+ *       of a row or block is taken as an fp32; beyond that range its scale is NaN.
+ *   X, Y of any type; residual and residual_out in X's type or TERN_F32
+ *       (TERN_ERR_DTYPE otherwise), both NULL for none; weight [K] of any type,
+ *       NULL for ones.  Y or codes may be NULL, not both; scales goes with codes.
+ *   residual_out may be the buffer of residual, or of X if the types are the
+ *       same; other buffers do not overlap.
+ *   K <= 65536 (TERN_ERR_SHAPE); eps >= 0 and finite (TERN_ERR_UNSUPPORTED).
+ * Every pointer needs the alignment of its element only.  Squares are summed in
+ * 64 bits.  A NaN or infinity reaches its own row only.
+ */
+tern_status tern_rms_norm(const void *X, tern_dtype x_dtype, const void *residual, tern_dtype r_dtype,
+                          const void *weight, tern_dtype w_dtype, void *residual_out, void *Y, tern_dtype y_dtype,
+                          int8_t *codes, float *scales, int32_t q_group, int64_t M, int64_t K, float eps,
+                          hipStream_t stream);
+
+/*
+ * tern_q8_quantize -- codes and scales of X[M,K] of any type, with q_group 0 for
+ * K <= 65536 (TERN_ERR_SHAPE).  tern_q8_dequant -- their values, rounded once to
+ * y_dtype.  Element alignment.
+ */
+tern_status tern_q8_quantize(const void *X, tern_dtype x_dtype, int8_t *codes, float *scales, int32_t q_group,
+                             int64_t M, int64_t K, hipStream_t stream);
+tern_status tern_q8_dequant(const int8_t *codes, const float *scales, int32_t q_group, void *Y, tern_dtype y_dtype,
+                            int64_t M, int64_t K, hipStream_t stream);
+
+/*
+ * tern_matmul_q8 -- tern_matmul with 8-bit activations:
+ *   Y[m,n] = sum over blocks g of 128 of x_scale[m,g] S[n,g] * sum over k in g of code[m,k] t[n,k]
+ * The inner sums are exact integers; the rest is fp32, rounded once.  Any codes
+ * from -128 to 127 and any scales.  packed_W, scales and group as tern_matmul;
+ * x_codes 16-byte, x_scales 4-byte aligned; K <= 2^23.  A NaN or infinite scale
+ * reaches its own row or column of Y only.
+ */
+tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t q_group, const uint8_t *packed_W,
+                           const uint16_t *scales, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,
+                           int32_t group, hipStream_t stream);
+
+/*
+ * tern_moe_route -- the experts of T tokens, and their weights, from a router's
+ * logits [T,E] of any type:
+ *   s = softmax of a token's logits, or sigmoid of each
+ *   c = s + bias (fp32 [E]); with bias NULL s, experts in the order of their logits
+ *   with groups > 1, groups of E / groups consecutive experts: only the experts of
+ *       the keep_groups groups with the largest sums of their group_best (1 or 2)
+ *       largest c are open
+ *   ids [T,top_k] int32: the top_k open experts, largest c first
+ *   weights [T,top_k] fp32: their s, divided by the sum of it over the taken ones
+ *       if renormalize is not 0 (0 where that sum is 0), times scale
+ * Ties go to the lowest index.  An expert whose logit or c is -inf is never taken:
+ * where fewer than top_k can be, the rest of ids is -1 with weight 0.  A NaN c
+ * counts as the largest; a softmax over a NaN or +inf has NaN weights.  c and the
+ * weights are formed in 64 bits, and the weights rounded once.
+ * groups divides E (TERN_ERR_GROUP); 1 <= keep_groups <= groups, group_best <= E /
+ * groups, 1 <= top_k <= keep_groups * (E / groups) (TERN_ERR_SHAPE); E <= 1024,
+ * top_k <= 32, groups <= 64 (TERN_ERR_UNSUPPORTED).  Element alignment.
+ */
+typedef enum { TERN_SCORE_SOFTMAX = 0, TERN_SCORE_SIGMOID = 1 } tern_score;
+tern_status tern_moe_route(const void *logits, tern_dtype l_dtype, const float *bias, int32_t *ids, float *weights,
+                           int64_t T, int64_t E, int64_t top_k, tern_score score, int64_t groups, int64_t keep_groups,
+                           int32_t group_best, int32_t renormalize, float scale, hipStream_t stream);
+
+/*
+ * tern_moe_routed -- tern_moe with its experts and weights given, ids [T,top_k]
+ * int32 and weights [T,top_k] fp32, as tern_moe_route leaves them:
+ *   y[t] = sum over j of weights[t,j] * Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])), e = ids[t,j]
+ * An id outside of [0, E) adds nothing; the same expert twice adds up.  Everything
+ * else as tern_moe, the workspace too; top_k <= 32 may exceed E.
+ */
+tern_status tern_moe_routed(const void *X, tern_dtype x_dtype, const int32_t *ids, const float *weights,
+                            const uint8_t *gate_up, const uint16_t *gate_up_scales, const uint8_t *down,
+                            const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E,
+                            int64_t top_k, int64_t H, int64_t F, int32_t group, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
 
 /*
  * tern_stream_copy -- calibration, not part of the method: stream `bytes`

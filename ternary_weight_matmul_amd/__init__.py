@@ -14,7 +14,11 @@ library raises: there is no fallback implementation.
     codes, exps = tern.mx_quantize(w)         # [N,K] -> 4-bit floats, a power-of-two scale per 32
     y = tern.mx_matmul(x, codes, exps)        # x . w^T, x in 16 bits
     y = tern.mx_matmul_mx(*tern.mx_quantize(x), codes, exps)    # both in 4 bits
+    codes, scales, h = tern.rms_norm_q8(x, w, residual=h)       # 8-bit activations
+    y = tern.matmul_q8(codes, scales, packed, weight_scales)    # and their product with ternary weights
     y = tern.moe(x, logits, gate_up, gate_up_scales, down, down_scales, top_k=8)    # ternary experts
+    ids, weights = tern.moe_route(logits, 8, score="sigmoid", bias=b, groups=8, keep_groups=4, group_best=2)
+    y = tern.moe_routed(x, ids, weights, gate_up, gate_up_scales, down, down_scales)
 """
 from __future__ import annotations
 
@@ -29,8 +33,10 @@ from ._lib import (  # noqa: F401
     library_path,
 )
 from .ops import (block_map, dequant, matmul, matmul_blockmap, matmul_blockmap_into, matmul_into,  # noqa: F401
-                  matmul_s8, matmul_s8_into, moe, moe_into, mx_dequant, mx_matmul, mx_matmul_into, mx_matmul_mx,
-                  mx_matmul_mx_into, mx_quantize, pack, quantize_scales, shard_columns, shard_k, stream_copy, unpack)
+                  matmul_q8, matmul_q8_into, matmul_s8, matmul_s8_into, moe, moe_into, moe_route, moe_routed,
+                  moe_routed_into, mx_dequant, mx_matmul, mx_matmul_into, mx_matmul_mx, mx_matmul_mx_into,
+                  mx_quantize, pack, q8_dequant, q8_quantize, quantize_scales, rms_norm, rms_norm_into, rms_norm_q8,
+                  shard_columns, shard_k, stream_copy, unpack)
 
 GROUP = 128
 MX_BLOCK = 32

@@ -83,6 +83,20 @@ def _load() -> ctypes.CDLL:
     L.tern_moe.argtypes = [vp, c_int, vp, c_int, vp, vp, vp, vp, vp, c_int, i64, i64, i64, i64, i64, i32, i32, vp,
                            ctypes.c_size_t, vp]
     L.tern_moe.restype = c_int
+    L.tern_moe_route.argtypes = [vp, c_int, vp, vp, vp, i64, i64, i64, c_int, i64, i64, i32, i32, ctypes.c_float, vp]
+    L.tern_moe_route.restype = c_int
+    L.tern_moe_routed.argtypes = [vp, c_int, vp, vp, vp, vp, vp, vp, vp, c_int, i64, i64, i64, i64, i64, i32, vp,
+                                  ctypes.c_size_t, vp]
+    L.tern_moe_routed.restype = c_int
+    L.tern_rms_norm.argtypes = [vp, c_int, vp, c_int, vp, c_int, vp, vp, c_int, vp, vp, i32, i64, i64, ctypes.c_float,
+                                vp]
+    L.tern_rms_norm.restype = c_int
+    L.tern_q8_quantize.argtypes = [vp, c_int, vp, vp, i32, i64, i64, vp]
+    L.tern_q8_quantize.restype = c_int
+    L.tern_q8_dequant.argtypes = [vp, vp, i32, vp, c_int, i64, i64, vp]
+    L.tern_q8_dequant.restype = c_int
+    L.tern_matmul_q8.argtypes = [vp, vp, i32, vp, vp, vp, c_int, i64, i64, i64, i32, vp]
+    L.tern_matmul_q8.restype = c_int
     L.tern_stream_copy.argtypes = [vp, vp, ctypes.c_uint64, vp]
     L.tern_stream_copy.restype = c_int
     return L

@@ -7,6 +7,8 @@
 #include "tern_kernels.h"
 #include "tern_moe.h"
 #include "tern_mx.h"
+#include "tern_q8.h"
+#include "tern_route.h"
 
 namespace {
 
@@ -15,6 +17,8 @@ constexpr int64_t kMaxK = int64_t(1) << 30;
 // Products with microscaled weights: offsets inside the rows of one workgroup are 32-bit (72 rows
 // of K / 2 bytes).
 constexpr int64_t kMxMaxK = int64_t(1) << 24;
+// Products with 8-bit activations: the same, 128 rows of K bytes.
+constexpr int64_t kQ8MaxK = int64_t(1) << 23;
 constexpr int64_t kMaxProduct = int64_t(1) << 62;
 constexpr size_t kGemvLdsLimit = 152 * 1024;
 
@@ -202,11 +206,71 @@ tern_status mx_product(const void *X, const uint8_t *XE, int x_dtype, const uint
     return from_hip(tern::mx_gemm_wins(a) ? tern::launch_mx_gemm(a) : tern::launch_mx_gemv(a));
 }
 
+// 8-bit activations [M,K]: their sizes and q_group; then their pointers, where there are any.
+tern_status check_q8_sizes(int32_t q_group, int64_t M, int64_t K) {
+    if (M < 0 || K < 0 || M > kMaxDim || K > kMaxK || !product_ok(M, K)) return TERN_ERR_SHAPE;
+    if (q_group != 0 && q_group != TERN_GROUP) return TERN_ERR_UNSUPPORTED;
+    if (q_group != 0 && K % q_group != 0) return TERN_ERR_GROUP;
+    return TERN_OK;
+}
+
+tern_status check_q8_pointers(const int8_t *codes, const float *scales) {
+    if (codes == nullptr || scales == nullptr) return TERN_ERR_NULL;
+    return aligned(scales, 4) ? TERN_OK : TERN_ERR_ALIGN;
+}
+
 bool moe_sizes_ok(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {
     if (T < 0 || E < 0 || top_k < 0 || H < 0 || F < 0) return false;
     if (T > kMaxDim || E > kMaxDim || top_k > kMaxDim || H > tern::kMoeMaxWidth || F > tern::kMoeMaxWidth)
         return false;
     return product_ok(2 * E, H * F) && product_ok(T, H) && product_ok(T, E);   // weights, values, logits
+}
+
+// tern_moe and, with ids and weights in place of the logits, tern_moe_routed.
+tern_status moe(const void *X, tern_dtype x_dtype, const void *logits, tern_dtype l_dtype, const int32_t *ids,
+                const float *weights, bool routed, const uint8_t *gate_up, const uint16_t *gate_up_scales,
+                const uint8_t *down, const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E,
+                int64_t top_k, int64_t H, int64_t F, int32_t group, int32_t renormalize, void *workspace,
+                size_t workspace_bytes, hipStream_t stream) {
+    if (!moe_sizes_ok(T, E, top_k, H, F) || top_k < 1 || (routed ? E < 1 : top_k > E))
+        return TERN_ERR_SHAPE;
+    if (group <= 0 || H % group != 0 || F % group != 0) return TERN_ERR_GROUP;
+    if (x_dtype != TERN_F16 && x_dtype != TERN_BF16) return TERN_ERR_DTYPE;
+    if (!known_dtype(l_dtype) || !known_dtype(y_dtype)) return TERN_ERR_DTYPE;
+    if (group != TERN_GROUP || E > tern::kMoeMaxExperts || top_k > tern::kMoeMaxTopK) return TERN_ERR_UNSUPPORTED;
+    if (T == 0 || H == 0) return TERN_OK;
+    if (Y == nullptr) return TERN_ERR_NULL;
+    if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
+    if (F == 0) return from_hip(tern::launch_fill_zero(Y, T * H * (int64_t)dtype_size(y_dtype), stream));
+    if ((routed ? ids == nullptr || weights == nullptr : logits == nullptr) || X == nullptr || gate_up == nullptr || gate_up_scales == nullptr || down == nullptr ||
+        down_scales == nullptr || workspace == nullptr)
+        return TERN_ERR_NULL;
+    if (!aligned(X, 16) || !aligned(logits, dtype_size(l_dtype)) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(gate_up, 16) || !aligned(down, 16) ||
+        !aligned(gate_up_scales, 2) || !aligned(down_scales, 2) || !aligned(workspace, 256))
+        return TERN_ERR_ALIGN;
+    if (workspace_bytes < tern::moe_workspace(T, top_k, H, F)) return TERN_ERR_SHAPE;
+    tern::MoeArgs a;
+    a.X = X;
+    a.x_dtype = dtype_index(x_dtype);
+    a.logits = logits;
+    a.l_dtype = dtype_index(l_dtype);
+    a.ids = ids;
+    a.weights = weights;
+    a.GU = gate_up;
+    a.GUS = gate_up_scales;
+    a.D = down;
+    a.DS = down_scales;
+    a.Y = Y;
+    a.y_dtype = dtype_index(y_dtype);
+    a.T = T;
+    a.E = E;
+    a.top_k = top_k;
+    a.H = H;
+    a.F = F;
+    a.renormalize = renormalize;
+    a.ws = workspace;
+    a.stream = stream;
+    return from_hip(tern::launch_moe(a));
 }
 
 }  // namespace
@@ -367,42 +431,155 @@ tern_status tern_moe(const void *X, tern_dtype x_dtype, const void *logits, tern
                      const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E, int64_t top_k,
                      int64_t H, int64_t F, int32_t group, int32_t renormalize, void *workspace,
                      size_t workspace_bytes, hipStream_t stream) {
-    if (!moe_sizes_ok(T, E, top_k, H, F) || top_k < 1 || top_k > E) return TERN_ERR_SHAPE;
-    if (group <= 0 || H % group != 0 || F % group != 0) return TERN_ERR_GROUP;
-    if (x_dtype != TERN_F16 && x_dtype != TERN_BF16) return TERN_ERR_DTYPE;
-    if (!known_dtype(l_dtype) || !known_dtype(y_dtype)) return TERN_ERR_DTYPE;
-    if (group != TERN_GROUP || E > tern::kMoeMaxExperts || top_k > tern::kMoeMaxTopK) return TERN_ERR_UNSUPPORTED;
-    if (T == 0 || H == 0) return TERN_OK;
-    if (Y == nullptr) return TERN_ERR_NULL;
-    if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
-    if (F == 0) return from_hip(tern::launch_fill_zero(Y, T * H * (int64_t)dtype_size(y_dtype), stream));
-    if (X == nullptr || logits == nullptr || gate_up == nullptr || gate_up_scales == nullptr || down == nullptr ||
-        down_scales == nullptr || workspace == nullptr)
-        return TERN_ERR_NULL;
-    if (!aligned(X, 16) || !aligned(logits, dtype_size(l_dtype)) || !aligned(gate_up, 16) || !aligned(down, 16) ||
-        !aligned(gate_up_scales, 2) || !aligned(down_scales, 2) || !aligned(workspace, 256))
+    return moe(X, x_dtype, logits, l_dtype, nullptr, nullptr, false, gate_up, gate_up_scales, down, down_scales, Y,
+               y_dtype, T, E, top_k, H, F, group, renormalize, workspace, workspace_bytes, stream);
+}
+
+tern_status tern_moe_routed(const void *X, tern_dtype x_dtype, const int32_t *ids, const float *weights,
+                            const uint8_t *gate_up, const uint16_t *gate_up_scales, const uint8_t *down,
+                            const uint16_t *down_scales, void *Y, tern_dtype y_dtype, int64_t T, int64_t E,
+                            int64_t top_k, int64_t H, int64_t F, int32_t group, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+    return moe(X, x_dtype, nullptr, TERN_F32, ids, weights, true, gate_up, gate_up_scales, down, down_scales, Y, y_dtype,
+               T, E, top_k, H, F, group, 0, workspace, workspace_bytes, stream);
+}
+
+tern_status tern_moe_route(const void *logits, tern_dtype l_dtype, const float *bias, int32_t *ids, float *weights,
+                           int64_t T, int64_t E, int64_t top_k, tern_score score, int64_t groups, int64_t keep_groups,
+                           int32_t group_best, int32_t renormalize, float scale, hipStream_t stream) {
+    if (T < 0 || E < 1 || T > kMaxDim || E > kMaxDim || !product_ok(T, E)) return TERN_ERR_SHAPE;
+    if (groups < 1 || E % groups != 0) return TERN_ERR_GROUP;
+    if (keep_groups < 1 || keep_groups > groups || group_best < 1 || group_best > 2) return TERN_ERR_SHAPE;
+    if ((groups > 1 && group_best > E / groups) || top_k < 1 || top_k > keep_groups * (E / groups)) return TERN_ERR_SHAPE;
+    if (!known_dtype(l_dtype)) return TERN_ERR_DTYPE;
+    if (score != TERN_SCORE_SOFTMAX && score != TERN_SCORE_SIGMOID) return TERN_ERR_UNSUPPORTED;
+    if (E > tern::kRouteMaxExperts || top_k > tern::kRouteMaxTopK || groups > tern::kRouteMaxGroups)
+        return TERN_ERR_UNSUPPORTED;
+    if (T == 0) return TERN_OK;
+    if (logits == nullptr || ids == nullptr || weights == nullptr) return TERN_ERR_NULL;
+    if (!aligned(logits, dtype_size(l_dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
         return TERN_ERR_ALIGN;
-    if (workspace_bytes < tern::moe_workspace(T, top_k, H, F)) return TERN_ERR_SHAPE;
-    tern::MoeArgs a;
-    a.X = X;
-    a.x_dtype = dtype_index(x_dtype);
+    tern::RouteArgs a;
     a.logits = logits;
     a.l_dtype = dtype_index(l_dtype);
-    a.GU = gate_up;
-    a.GUS = gate_up_scales;
-    a.D = down;
-    a.DS = down_scales;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.T = T;
+    a.E = (int)E;
+    a.top_k = (int)top_k;
+    a.sigmoid = score == TERN_SCORE_SIGMOID;
+    a.groups = (int)groups;
+    a.keep = (int)keep_groups;
+    a.best = group_best;
+    a.renormalize = renormalize;
+    a.scale = scale;
+    a.stream = stream;
+    return from_hip(tern::launch_route(a));
+}
+
+tern_status tern_rms_norm(const void *X, tern_dtype x_dtype, const void *residual, tern_dtype r_dtype,
+                          const void *weight, tern_dtype w_dtype, void *residual_out, void *Y, tern_dtype y_dtype,
+                          int8_t *codes, float *scales, int32_t q_group, int64_t M, int64_t K, float eps,
+                          hipStream_t stream) {
+    const bool coded = codes != nullptr || scales != nullptr, added = residual != nullptr || residual_out != nullptr;
+    tern_status st = check_q8_sizes(coded ? q_group : 0, M, K);
+    if (st != TERN_OK) return st;
+    if (K > tern::kNormMaxK) return TERN_ERR_SHAPE;
+    if (!known_dtype(x_dtype) || (added && r_dtype != x_dtype && r_dtype != TERN_F32)) return TERN_ERR_DTYPE;
+    if ((weight != nullptr && !known_dtype(w_dtype)) || (Y != nullptr && !known_dtype(y_dtype))) return TERN_ERR_DTYPE;
+    if (!(eps >= 0.f && eps <= 3.402823466e38f)) return TERN_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return TERN_OK;
+    if (X == nullptr || (Y == nullptr && !coded)) return TERN_ERR_NULL;
+    if (added && (residual == nullptr || residual_out == nullptr)) return TERN_ERR_NULL;
+    if (coded && (st = check_q8_pointers(codes, scales)) != TERN_OK) return st;
+    if (!aligned(X, dtype_size(x_dtype)) || (Y != nullptr && !aligned(Y, dtype_size(y_dtype))) ||
+        (weight != nullptr && !aligned(weight, dtype_size(w_dtype))) ||
+        (added && (!aligned(residual, dtype_size(r_dtype)) || !aligned(residual_out, dtype_size(r_dtype)))))
+        return TERN_ERR_ALIGN;
+    tern::NormArgs a{};
+    a.X = X;
+    a.x_dtype = dtype_index(x_dtype);
+    a.R = residual;
+    a.r_dtype = added ? dtype_index(r_dtype) : 0;
+    a.W = weight;
+    a.w_dtype = weight != nullptr ? dtype_index(w_dtype) : 0;
+    a.H = residual_out;
+    a.Y = Y;
+    a.y_dtype = Y != nullptr ? dtype_index(y_dtype) : 0;
+    a.Q = codes;
+    a.S = scales;
+    a.grouped = coded && q_group != 0;
+    a.normalize = 1;
+    a.M = M;
+    a.K = K;
+    a.eps = eps;
+    a.stream = stream;
+    return from_hip(tern::launch_norm(a));
+}
+
+tern_status tern_q8_quantize(const void *X, tern_dtype x_dtype, int8_t *codes, float *scales, int32_t q_group,
+                             int64_t M, int64_t K, hipStream_t stream) {
+    tern_status st = check_q8_sizes(q_group, M, K);
+    if (st != TERN_OK) return st;
+    if (q_group == 0 && K > tern::kNormMaxK) return TERN_ERR_SHAPE;
+    if (!known_dtype(x_dtype)) return TERN_ERR_DTYPE;
+    if (M == 0 || K == 0) return TERN_OK;
+    if (X == nullptr) return TERN_ERR_NULL;
+    if ((st = check_q8_pointers(codes, scales)) != TERN_OK) return st;
+    if (!aligned(X, dtype_size(x_dtype))) return TERN_ERR_ALIGN;
+    tern::NormArgs a{};
+    a.X = X;
+    a.x_dtype = dtype_index(x_dtype);
+    a.Q = codes;
+    a.S = scales;
+    a.M = q_group != 0 ? M * (K / q_group) : M;   // blocks are rows of their own
+    a.K = q_group != 0 ? q_group : K;
+    a.stream = stream;
+    return from_hip(tern::launch_norm(a));
+}
+
+tern_status tern_q8_dequant(const int8_t *codes, const float *scales, int32_t q_group, void *Y, tern_dtype y_dtype,
+                            int64_t M, int64_t K, hipStream_t stream) {
+    tern_status st = check_q8_sizes(q_group, M, K);
+    if (st != TERN_OK) return st;
+    if (!known_dtype(y_dtype)) return TERN_ERR_DTYPE;
+    if (M == 0 || K == 0) return TERN_OK;
+    if (Y == nullptr) return TERN_ERR_NULL;
+    if ((st = check_q8_pointers(codes, scales)) != TERN_OK) return st;
+    if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
+    const int64_t width = q_group != 0 ? q_group : K;
+    return from_hip(tern::launch_q8_dequant(codes, scales, Y, dtype_index(y_dtype), M * (K / width), width, stream));
+}
+
+tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t q_group, const uint8_t *packed_W,
+                           const uint16_t *scales, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,
+                           int32_t group, hipStream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kQ8MaxK) return TERN_ERR_SHAPE;
+    if (!product_ok(M, N)) return TERN_ERR_SHAPE;
+    if (group <= 0 || K % group != 0) return TERN_ERR_GROUP;
+    if (!known_dtype(y_dtype)) return TERN_ERR_DTYPE;
+    if (group != TERN_GROUP || (q_group != 0 && q_group != TERN_GROUP)) return TERN_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return TERN_OK;
+    if (Y == nullptr) return TERN_ERR_NULL;
+    if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
+    if (K == 0) return from_hip(tern::launch_fill_zero(Y, M * N * (int64_t)dtype_size(y_dtype), stream));
+    if (x_codes == nullptr || x_scales == nullptr || packed_W == nullptr || scales == nullptr) return TERN_ERR_NULL;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 4) || !aligned(packed_W, 16) || !aligned(scales, 2))
+        return TERN_ERR_ALIGN;
+    tern::Q8Args a;
+    a.Q = x_codes;
+    a.XS = x_scales;
+    a.grouped = q_group != 0;
+    a.W = packed_W;
+    a.S = scales;
     a.Y = Y;
     a.y_dtype = dtype_index(y_dtype);
-    a.T = T;
-    a.E = E;
-    a.top_k = top_k;
-    a.H = H;
-    a.F = F;
-    a.renormalize = renormalize;
-    a.ws = workspace;
+    a.M = M;
+    a.N = N;
+    a.K = K;
     a.stream = stream;
-    return from_hip(tern::launch_moe(a));
+    return from_hip(tern::launch_q8_gemm(a));
 }
 
 }  // extern "C"

@@ -19,6 +19,8 @@ struct MoeArgs {
     int x_dtype;                 // 0 = fp16, 1 = bf16
     const void *logits;          // [T,E]
     int l_dtype;                 // 0 = fp16, 1 = bf16, 2 = fp32
+    const int *ids;              // [T,top_k] experts with
+    const float *weights;        // [T,top_k] weights in place of the logits, or null
     const uint8_t *GU;           // [E,2F,H/4]
     const uint16_t *GUS;         // [E,2F,H/128]
     const uint8_t *D;            // [E,H,F/4]

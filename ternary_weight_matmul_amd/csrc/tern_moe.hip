@@ -18,6 +18,8 @@
 // terms are those of v / 4, so that no term and no product with +-2 leaves the
 // fp32 range before v does.
 //
+// S and w may be given instead, from any router.
+//
 // Launches.  Up to kMoeSmall tokens take two: the up kernel, whose workgroups
 // each route every token anew (a microsecond, against two for a launch of its
 // own), and a down kernel whose workgroups own output rows, go through all
@@ -52,6 +54,7 @@
 #include "tern_device.h"
 #include "tern_launch.h"
 #include "tern_moe.h"
+#include "tern_route_device.h"
 
 namespace tern {
 
@@ -66,46 +69,6 @@ typedef float float4v_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ---- routing ------------------------------------------------------------------
-
-__device__ __forceinline__ float load_logit(const void *l, int dtype, int64_t i) {
-    if (dtype == 2) return static_cast<const float *>(l)[i];
-    if (dtype == 1) return __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t *>(l)[i] << 16);
-    return f16_bits_to_float(static_cast<const uint16_t *>(l)[i]);
-}
-
-// Unsigned key in the order of the values, never 0: NaN above all, -0 equal to 0.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v != v ? __builtin_bit_cast(float, 0x7FC00000u) : v + 0.0f);
-    return (u >> 31) ? ~u : u | 0x80000000u;
-}
-
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __builtin_bit_cast(float, (k >> 31) ? k & 0x7FFFFFFFu : ~k);
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
-}
-
-// Maximum over the wave, the same for every lane.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = max(v, dpp<0x128>(v));   // rotations within rows of 16
-    v = max(v, dpp<0x124>(v));
-    v = max(v, dpp<0x122>(v));
-    v = max(v, dpp<0x121>(v));
-    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
-    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-    return max(max(a, b), max(c, d));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-    v = row16_sum(v);
-    auto lane_of = [&](int l) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
-    };
-    return (lane_of(0) + lane_of(16)) + (lane_of(32) + lane_of(48));
-}
 
 // One wave routes one token: lane j < top_k gets the j-th expert and its
 // weight (-1 and 0 where there is none).  E <= 64 R.
@@ -162,6 +125,29 @@ __device__ __forceinline__ void route_any(const void *logits, int l_dtype, int64
     else route_token<16>(logits, l_dtype, row, E, top_k, renorm, lane, id, weight);
 }
 
+// The same where the experts and weights are given.  Indices outside of [0, E) are none; an expert
+// that is there more than once is taken once, with the sum of its weights.
+__device__ __forceinline__ void given_token(const int *ids, const float *weights, int64_t row, int E, int top_k,
+                                            int lane, int &id, float &weight) {
+    id = -1, weight = 0.f;
+    if (lane < top_k) {
+        id = ids[row * top_k + lane];
+        weight = weights[row * top_k + lane];
+        if ((unsigned)id >= (unsigned)E) id = -1, weight = 0.f;
+    }
+    for (int j = 0; j < top_k; ++j) {
+        const int e = __builtin_amdgcn_readlane(id, j);
+        const bool mine = e >= 0 && id == e;
+        const uint64_t same = __ballot(mine);
+        if (__popcll(same) < 2) continue;
+        const float total = wave_sum(mine ? weight : 0.f);
+        if (mine) {
+            if (lane == j) weight = total;   // the first: those before it are done with
+            else id = -1, weight = 0.f;
+        }
+    }
+}
+
 // Index of the n-th set bit over `words` words, -1 if there are fewer.
 __device__ __forceinline__ int nth_bit(const uint32_t *bits, int words, int n) {
     for (int w = 0; w < words; ++w) {
@@ -193,7 +179,8 @@ struct Plan {
 
 // More tokens: routing and the lists, by one workgroup of 16 waves.
 __global__ __launch_bounds__(1024) void moe_plan_kernel(const void *__restrict__ logits, int l_dtype, int T, int E,
-                                                        int top_k, int renorm, int slots, Plan plan) {
+                                                        int top_k, int renorm, const int *__restrict__ given,
+                                                        const float *__restrict__ given_weights, int slots, Plan plan) {
     __shared__ int ids[kMoeChunk * kMoeMaxTopK];
     __shared__ int count[kMoeMaxExperts], place[kMoeMaxExperts];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -202,7 +189,8 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const void *__restrict__
     for (int t = wave; t < T; t += 16) {
         int id;
         float w;
-        route_any(logits, l_dtype, t, E, top_k, renorm != 0, lane, id, w);
+        if (given != nullptr) given_token(given, given_weights, t, E, top_k, lane, id, w);
+        else route_any(logits, l_dtype, t, E, top_k, renorm != 0, lane, id, w);
         if (lane < top_k) {
             ids[t * top_k + lane] = id;
             plan.ids[t * top_k + lane] = id;
@@ -432,13 +420,6 @@ __host__ __device__ constexpr int sums_floats() { return 2 * SETS * Q * 64; }
 template <int SETS>
 __host__ __device__ constexpr int ops_bytes(int groups) { return (groups + 3) / 4 * SETS * 4096; }
 
-// The compiler keeps the wave's LDS accesses on their sides.
-__device__ __forceinline__ void wave_order() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 template <int SETS, int Q>
 __device__ __forceinline__ void clear(float4v_t (&acc)[Q][SETS]) {
 #pragma unroll
@@ -511,7 +492,9 @@ template <int AT, int SETS, int Q, int G, bool SMALL>
 __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__restrict__ X, const void *__restrict__ logits,
                                                              int l_dtype, const uint8_t *__restrict__ GU,
                                                              const uint16_t *__restrict__ GUS, Plan plan, int T, int E,
-                                                             int top_k, int renorm, int H, int F, int terms) {
+                                                             int top_k, int renorm, const int *__restrict__ given,
+                                                             const float *__restrict__ given_weights, int H, int F,
+                                                             int terms) {
     static_assert(Q % 2 == 0, "gate and up quads");
     constexpr int ROWS = SETS * rows_per_set(AT);
     static_assert(!SMALL || ROWS >= kMoeSmall, "a slot a token");
@@ -533,7 +516,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void moe_up_kernel(const char *__re
         if (wave < T) {   // T <= 4
             int id;
             float w;
-            route_any(logits, l_dtype, wave, E, top_k, renorm != 0, lane, id, w);
+            if (given != nullptr) given_token(given, given_weights, wave, E, top_k, lane, id, w);
+            else route_any(logits, l_dtype, wave, E, top_k, renorm != 0, lane, id, w);
             if (lane < top_k) {
                 ids[wave * top_k + lane] = id;
                 weights[wave * top_k + lane] = w;
@@ -857,7 +841,7 @@ hipError_t launch_up(const MoeArgs &a, const Plan &plan, int slots) {
     const hipError_t e = raise_lds_limit<kern>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, g, b, lds, a.stream, static_cast<const char *>(a.X), a.logits, a.l_dtype, a.GU, a.GUS, plan,
-                       (int)a.T, (int)a.E, (int)a.top_k, a.renormalize, (int)a.H, (int)a.F, hidden_terms(a));
+                       (int)a.T, (int)a.E, (int)a.top_k, a.renormalize, a.ids, a.weights, (int)a.H, (int)a.F, hidden_terms(a));
     return hipGetLastError();
 }
 
@@ -936,7 +920,7 @@ hipError_t launch_chunk(const MoeArgs &a) {
         return down_small<AT, 2>(a, plan);
     }
     hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.logits, a.l_dtype, (int)a.T, (int)a.E,
-                       (int)a.top_k, a.renormalize, slots, plan);
+                       (int)a.top_k, a.renormalize, a.ids, a.weights, slots, plan);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     // A second set of slots once the experts have more than two tokens in the mean.
@@ -963,7 +947,8 @@ hipError_t launch_moe(const MoeArgs &a0) {
     for (int64_t t = 0; t < a0.T; t += kMoeChunk) {
         a.T = a0.T - t < kMoeChunk ? a0.T - t : kMoeChunk;
         a.X = static_cast<const char *>(a0.X) + t * a.H * 2;
-        a.logits = static_cast<const char *>(a0.logits) + t * a.E * lsize;
+        if (a0.ids != nullptr) a.ids = a0.ids + t * a.top_k, a.weights = a0.weights + t * a.top_k;
+        else a.logits = static_cast<const char *>(a0.logits) + t * a.E * lsize;
         a.Y = static_cast<char *>(a0.Y) + t * a.H * ysize;
         const hipError_t e = hidden_terms(a) == 3 ? launch_chunk<3>(a) : launch_chunk<2>(a);
         if (e != hipSuccess) return e;

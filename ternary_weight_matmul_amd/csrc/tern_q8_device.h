@@ -1,0 +1,67 @@
+// tern_q8_device.h -- ternary weights as 8-bit operands, shared by the products
+// with 8-bit activations.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tern_buffer.h"
+#include "tern_device.h"
+
+namespace tern {
+
+typedef int int4v_t __attribute__((ext_vector_type(4)));
+typedef float float4v_t __attribute__((ext_vector_type(4)));
+
+// 32 codes (two words of 16) -> 32 int8 in {-1, 0, +1} in their own order, which is that of the
+// activations' bytes in memory: no byte of those is moved anywhere.
+//
+// A word is a 4 x 4 matrix of 2-bit fields, byte j and place i in it for weight 4 j + i.  A shift
+// and a mask take one place of all bytes, weights i, 4 + i, 8 + i, 12 + i; so the matrix is
+// transposed first, two swaps of off-diagonal fields (quarters, then within them), after which
+// they are weights 4 i .. 4 i + 3.  A byte permutation then looks each code up in {0, 1, -1, 0}.
+__device__ __forceinline__ void decode32(uint2 code, int4v_t &a, int4v_t &b) {
+    uint64_t x = code.x | (uint64_t)code.y << 32;
+    uint64_t t = (x ^ (x >> 6)) & 0x00CC00CC00CC00CCull;   // field i0 with bit 0 of the byte
+    x ^= t ^ (t << 6);
+    t = (x ^ (x >> 12)) & 0x0000F0F00000F0F0ull;           // and the bits 1
+    x ^= t ^ (t << 12);
+    constexpr uint32_t VALUES = 0x00FF0100u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t f = (x >> (2 * i)) & 0x0303030303030303ull;
+        a[i] = (int)__builtin_amdgcn_perm(0u, VALUES, (uint32_t)f);
+        b[i] = (int)__builtin_amdgcn_perm(0u, VALUES, (uint32_t)(f >> 32));
+    }
+}
+
+__device__ __forceinline__ int4v_t mfma_i8(const int4v_t &a, const int4v_t &b, const int4v_t &c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// `count` of 4 consecutive outputs from index `at` on; vec: all 4 at once where they are there.
+__device__ __forceinline__ void store4(void *Y, int y_dtype, int64_t at, const float4v_t &d, int count, int vec) {
+    if (vec && count == 4) {
+        if (y_dtype == 2) {
+            *reinterpret_cast<float4v_t *>(static_cast<float *>(Y) + at) = d;
+        } else if (y_dtype == 1) {
+            const bf162_t a = {(__bf16)d[0], (__bf16)d[1]}, b = {(__bf16)d[2], (__bf16)d[3]};
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(Y) + at) =
+                make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+        } else {
+            const half2_t a = {(_Float16)d[0], (_Float16)d[1]}, b = {(_Float16)d[2], (_Float16)d[3]};
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(Y) + at) =
+                make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+        }
+        return;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (v < count) {
+            if (y_dtype == 2) store_out<2>(Y, at + v, d[v]);
+            else if (y_dtype == 1) store_out<1>(Y, at + v, d[v]);
+            else store_out<0>(Y, at + v, d[v]);
+        }
+}
+
+}  // namespace tern

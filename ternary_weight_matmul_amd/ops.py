@@ -340,11 +340,13 @@ def mx_matmul_mx(x_codes: torch.Tensor, x_exps: torch.Tensor, codes: torch.Tenso
 
 # --- mixture of ternary experts -------------------------------------------------
 
-def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
-             down: torch.Tensor, down_scales: torch.Tensor, out: torch.Tensor, top_k: int,
-             renormalize: bool = True, group: int = 128) -> torch.Tensor:
-    """out [T,H] = the mixture-of-experts layer of tern_moe: x [T,H] fp16/bf16, logits [T,E],
-    gate_up [E,2F,H/4] and down [E,H,F/4] packed codes, their fp16 scales one per 128."""
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+
+
+def _need_experts(x: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor, down: torch.Tensor,
+                  down_scales: torch.Tensor, out: torch.Tensor, group: int):
+    """(GPU index, T, E, H, F) of an expert layer's operands."""
     device = _need_matrix(x, "x", _FLOAT16S)
     if gate_up.dim() != 3 or down.dim() != 3:
         raise ValueError("gate_up must be [E, 2F, H/4] and down [E, H, F/4]")
@@ -352,12 +354,21 @@ def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_
         raise ValueError("group must be positive")
     T, H = x.shape
     E, F = gate_up.shape[0], down.shape[2] * 4
-    _need_at(logits, "logits", device, _FLOATS, (T, E))
     _need_at(gate_up, "gate_up", device, _U8, (E, 2 * F, H // 4))
     _need_at(gate_up_scales, "gate_up_scales", device, _F16, (E, 2 * F, H // group))
     _need_at(down, "down", device, _U8, (E, H, F // 4))
     _need_at(down_scales, "down_scales", device, _F16, (E, H, F // group))
     _need_at(out, "out", device, _FLOATS, (T, H))
+    return device, T, E, H, F
+
+
+def moe_into(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_scales: torch.Tensor,
+             down: torch.Tensor, down_scales: torch.Tensor, out: torch.Tensor, top_k: int,
+             renormalize: bool = True, group: int = 128) -> torch.Tensor:
+    """out [T,H] = the mixture-of-experts layer of tern_moe: x [T,H] fp16/bf16, logits [T,E],
+    gate_up [E,2F,H/4] and down [E,H,F/4] packed codes, their fp16 scales one per 128."""
+    device, T, E, H, F = _need_experts(x, gate_up, gate_up_scales, down, down_scales, out, group)
+    _need_at(logits, "logits", device, _FLOATS, (T, E))
     nbytes = lib.tern_moe_workspace(T, E, top_k, H, F)
     # allocated on the current stream: torch's allocator keeps it for this call until that stream
     # has passed it, and inside a graph capture it belongs to the graph
@@ -376,6 +387,188 @@ def moe(x: torch.Tensor, logits: torch.Tensor, gate_up: torch.Tensor, gate_up_sc
     outputs the hidden values keep all their bits, with 16-bit outputs 16 of them in less time."""
     out = x.new_empty(x.shape, dtype=out_dtype)
     return moe_into(x, logits, gate_up, gate_up_scales, down, down_scales, out, top_k, renormalize, group)
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+              groups: int = 1, keep_groups: int = 1, group_best: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """The experts ids int32 [T,top_k] of every token and their weights fp32 [T,top_k] from logits [T,E]
+    (tern_moe_route): softmax or sigmoid scores, chosen by score + bias (fp32 [E]) among the keep_groups of
+    `groups` groups of consecutive experts whose group_best largest add up to the most."""
+    index = _need_matrix(logits, "logits", _FLOATS)
+    T, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if bias is not None:
+        _need_at(bias, "bias", index, _F32, (E,))
+    if not 1 <= top_k <= max(E, 1):
+        raise ValueError(f"top_k must be in [1, {E}], got {top_k}")
+    ids = logits.new_empty((T, top_k), dtype=torch.int32)
+    weights = logits.new_empty((T, top_k), dtype=torch.float32)
+    _launch(lib.tern_moe_route, "tern_moe_route", logits, logits.data_ptr(), _TORCH_CODE[logits.dtype],
+            bias.data_ptr() if bias is not None else 0, ids.data_ptr(), weights.data_ptr(), T, E, top_k, _SCORES[score],
+            groups, keep_groups, group_best, int(renormalize), scale)
+    return ids, weights
+
+
+def moe_routed_into(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: torch.Tensor,
+                    gate_up_scales: torch.Tensor, down: torch.Tensor, down_scales: torch.Tensor, out: torch.Tensor,
+                    group: int = 128) -> torch.Tensor:
+    """out [T,H] = moe_into with the experts ids int32 [T,k] and their weights fp32 [T,k] given (from
+    moe_route, or any router)."""
+    device, T, E, H, F = _need_experts(x, gate_up, gate_up_scales, down, down_scales, out, group)
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be [T, k], got {tuple(ids.shape)}")
+    top_k = ids.shape[1]
+    _need_at(ids, "ids", device, _I32, (T, top_k))
+    _need_at(weights, "weights", device, _F32, (T, top_k))
+    nbytes = lib.tern_moe_workspace(T, E, top_k, H, F)
+    ws = x.new_empty((nbytes,), dtype=torch.uint8)   # as in moe_into
+    _launch(lib.tern_moe_routed, "tern_moe_routed", x, x.data_ptr(), _TORCH_CODE[x.dtype], ids.data_ptr(),
+            weights.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(),
+            out.data_ptr(), _TORCH_CODE[out.dtype], T, E, top_k, H, F, group, ws.data_ptr(), nbytes)
+    return out
+
+
+def moe_routed(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: torch.Tensor,
+               gate_up_scales: torch.Tensor, down: torch.Tensor, down_scales: torch.Tensor,
+               out_dtype: Optional[torch.dtype] = None, group: int = 128) -> torch.Tensor:
+    """The layer's outputs [T,H] (of x's type unless out_dtype is given) as a new tensor."""
+    out = x.new_empty(x.shape, dtype=out_dtype)
+    return moe_routed_into(x, ids, weights, gate_up, gate_up_scales, down, down_scales, out, group)
+
+
+# --- norms and 8-bit activations --------------------------------------------------
+
+_I8 = (torch.int8,)
+
+
+def _q_shape(M: int, K: int, group: int):
+    """Shape of the scales of 8-bit activations [M,K]: one per row (group 0) or per `group` of a row."""
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (a scale per row) or 128")
+    if group and K % group != 0:
+        raise ValueError(f"K = {K} must be a multiple of the group of 128")
+    return (M, K // group) if group else (M, 1)
+
+
+def _need_q8(codes: torch.Tensor, scales: torch.Tensor, index: int):
+    """(M, K, group) of 8-bit activations held as codes [M,K] and scales [M,1] or [M,K/128] on GPU `index`."""
+    _need_matrix(codes, "codes", _I8)
+    M, K = codes.shape
+    if scales.dim() != 2 or scales.shape[0] != M or not (scales.shape[1] == 1 or scales.shape[1] * 128 == K):
+        raise ValueError(f"scales must be [M, 1] or [M, K/128] for codes {tuple(codes.shape)}, got {tuple(scales.shape)}")
+    _need_at(scales, "scales", index, _F32, scales.shape)
+    return M, K, 0 if scales.shape[1] == 1 else 128
+
+
+def rms_norm_into(x: torch.Tensor, weight: Optional[torch.Tensor], out: Optional[torch.Tensor] = None,
+                  codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  residual: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None) -> None:
+    """The norm of tern_rms_norm of x [M,K] into out [M,K], codes [M,K] with scales, or both.  With a
+    residual [M,K] (x's type or fp32) the norm is that of x + residual, which goes to residual_out
+    (residual itself if not given)."""
+    index = _need_matrix(x, "x", _FLOATS)
+    M, K = x.shape
+    if out is None and codes is None:
+        raise ValueError("out or codes must be given")
+    if weight is not None:
+        _need_at(weight, "weight", index, _FLOATS, (K,))
+    if out is not None:
+        _need_at(out, "out", index, _FLOATS, (M, K))
+    group = 0
+    if codes is not None:
+        if scales is None:
+            raise ValueError("scales must be given with codes")
+        _need_at(codes, "codes", index, _I8, (M, K))
+        group = _need_q8(codes, scales, index)[2]
+    elif scales is not None:
+        raise ValueError("codes must be given with scales")
+    if residual is not None:
+        _need_at(residual, "residual", index, (x.dtype, torch.float32), (M, K))
+        residual_out = residual if residual_out is None else residual_out
+        _need_at(residual_out, "residual_out", index, (residual.dtype,), (M, K))
+    elif residual_out is not None:
+        raise ValueError("residual must be given with residual_out")
+    _launch(lib.tern_rms_norm, "tern_rms_norm", x, x.data_ptr(), _TORCH_CODE[x.dtype],
+            residual.data_ptr() if residual is not None else 0, _TORCH_CODE[residual.dtype] if residual is not None else 0,
+            weight.data_ptr() if weight is not None else 0, _TORCH_CODE[weight.dtype] if weight is not None else 0,
+            residual_out.data_ptr() if residual_out is not None else 0, out.data_ptr() if out is not None else 0,
+            _TORCH_CODE[out.dtype] if out is not None else 0, codes.data_ptr() if codes is not None else 0,
+            scales.data_ptr() if scales is not None else 0, group, M, K, eps)
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None):
+    """y = h / sqrt(mean(h^2) + eps) * weight of every row, h = x [M,K]; y in x's type unless out_dtype is
+    given.  With a residual [M,K] h is x + residual in the residual's type, and (y, h) is returned."""
+    out = x.new_empty(x.shape, dtype=out_dtype)
+    h = torch.empty_like(residual) if residual is not None else None
+    rms_norm_into(x, weight, out=out, eps=eps, residual=residual, residual_out=h)
+    return out if h is None else (out, h)
+
+
+def rms_norm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                residual: Optional[torch.Tensor] = None, group: int = 0):
+    """rms_norm with the outputs as 8-bit activations: (codes int8 [M,K], scales fp32 [M,1], or [M,K/128]
+    with group 128), and h with a residual."""
+    _need_matrix(x, "x", _FLOATS)
+    codes = x.new_empty(x.shape, dtype=torch.int8)
+    scales = x.new_empty(_q_shape(*x.shape, group), dtype=torch.float32)
+    h = torch.empty_like(residual) if residual is not None else None
+    rms_norm_into(x, weight, codes=codes, scales=scales, eps=eps, residual=residual, residual_out=h)
+    return (codes, scales) if h is None else (codes, scales, h)
+
+
+def q8_quantize(x: torch.Tensor, group: int = 0):
+    """x [M,K] -> 8-bit activations (codes int8 [M,K], scales fp32 [M,1], or [M,K/128] with group 128):
+    127 x / a rounded to nearest even, a the largest magnitude of the row or block (tern_q8_quantize)."""
+    _need_matrix(x, "x", _FLOATS)
+    M, K = x.shape
+    codes = x.new_empty((M, K), dtype=torch.int8)
+    scales = x.new_empty(_q_shape(M, K, group), dtype=torch.float32)
+    _launch(lib.tern_q8_quantize, "tern_q8_quantize", x, x.data_ptr(), _TORCH_CODE[x.dtype], codes.data_ptr(),
+            scales.data_ptr(), group, M, K)
+    return codes, scales
+
+
+def q8_dequant(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The values codes * scales of 8-bit activations as a new tensor."""
+    M, K, group = _need_q8(codes, scales, codes.get_device())
+    if out_dtype not in _TORCH_CODE:
+        raise TypeError("out_dtype must be float32, bfloat16 or float16")
+    out = codes.new_empty((M, K), dtype=out_dtype)
+    _launch(lib.tern_q8_dequant, "tern_q8_dequant", codes, codes.data_ptr(), scales.data_ptr(), group, out.data_ptr(),
+            _TORCH_CODE[out_dtype], M, K)
+    return out
+
+
+def matmul_q8_into(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tensor, weight_scales: torch.Tensor,
+                   out: torch.Tensor, group: int = 128) -> torch.Tensor:
+    """out[M,N] = X . (T*S)^T with X held as 8-bit activations, W as packed codes [N,K/4] and fp16 scales
+    [N,K/group]."""
+    index = codes.get_device()
+    M, K, q_group = _need_q8(codes, scales, index)
+    if group <= 0:
+        raise ValueError("group must be positive")
+    if packed.dim() != 2 or packed.shape[1] * 4 != K:
+        raise ValueError(f"shape mismatch: codes {tuple(codes.shape)}, packed {tuple(packed.shape)}")
+    N = packed.shape[0]
+    _need_at(packed, "packed", index, _U8, (N, K // 4))
+    _need_at(weight_scales, "weight_scales", index, _F16, (N, K // group))
+    _need_at(out, "out", index, _FLOATS, (M, N))
+    _launch(lib.tern_matmul_q8, "tern_matmul_q8", codes, codes.data_ptr(), scales.data_ptr(), q_group, packed.data_ptr(),
+            weight_scales.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, group)
+    return out
+
+
+def matmul_q8(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tensor, weight_scales: torch.Tensor,
+              out_dtype: torch.dtype = torch.bfloat16, group: int = 128) -> torch.Tensor:
+    """Y[M,N] = X . (T*S)^T with X held as 8-bit activations (from rms_norm_q8 or q8_quantize); a new tensor."""
+    out = codes.new_empty((codes.shape[0], packed.shape[0]), dtype=out_dtype)
+    return matmul_q8_into(codes, scales, packed, weight_scales, out, group)
 
 
 # --- one GPU's share of a sharded layer (no communication here) -------------
