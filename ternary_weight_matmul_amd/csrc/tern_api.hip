@@ -567,6 +567,12 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
     if (x_codes == nullptr || x_scales == nullptr || packed_W == nullptr || scales == nullptr) return TERN_ERR_NULL;
     if (!aligned(x_codes, 16) || !aligned(x_scales, 4) || !aligned(packed_W, 16) || !aligned(scales, 2))
         return TERN_ERR_ALIGN;
+    if (M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3)) {
+        tern::GemmArgs g = make_args(x_codes, TERN_BF16, packed_W, scales, nullptr, x_scales, Y, y_dtype, M, N, K, stream);
+        g.x_dtype = 3;
+        g.x_grouped = q_group != 0;
+        return from_hip(tern::launch_gemv_fp4(g));
+    }
     tern::Q8Args a;
     a.Q = x_codes;
     a.XS = x_scales;
@@ -579,7 +585,7 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
     a.N = N;
     a.K = K;
     a.stream = stream;
-    return from_hip(tern::launch_q8_gemm(a));
+    return from_hip(tern::q8_rows_fits(a) ? tern::launch_q8_rows(a) : tern::launch_q8_gemm(a));
 }
 
 }  // extern "C"

@@ -96,6 +96,27 @@ __device__ __forceinline__ void split8(const uint4 &q, uint32_t eh, uint32_t el,
     lo_odd = __builtin_amdgcn_perm(lb23, lb01, 0x07050301u);
 }
 
+// The same for 8 int8 activations (4 in each word), with scale 1 for both terms: hi is the value
+// rounded to 4 significant bits, at most 128, and lo what is left, at most 4.  Every product of a
+// term with +-2 is an integer of up to 256, so that nothing is cut off in their sums.
+__device__ __forceinline__ void split8_codes(uint32_t w0, uint32_t w1, uint32_t &hi_even, uint32_t &hi_odd,
+                                             uint32_t &lo_even, uint32_t &lo_odd) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)((i < 4 ? w0 : w1) >> (8 * (i & 3)));
+    // evens, then odds, as bytes of a word
+    auto pack = [](float a, float b, float c, float d) {
+        int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    };
+    hi_even = pack(v[0], v[2], v[4], v[6]);
+    hi_odd = pack(v[1], v[3], v[5], v[7]);
+    const fp4_float2_t e0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi_even, false), e1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi_even, true);
+    const fp4_float2_t o0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi_odd, false), o1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi_odd, true);
+    lo_even = pack(v[0] - e0[0], v[2] - e0[1], v[4] - e1[0], v[6] - e1[1]);
+    lo_odd = pack(v[1] - o0[0], v[3] - o0[1], v[5] - o1[0], v[7] - o1[1]);
+}
+
 // D = A * B + C on the matrix cores: A e4m3 with per-lane block scale sa
 // (E8M0), B e2m1 (scale 1).
 __device__ __forceinline__ fp4_float4_t mfma_f8f4(const fp4_int8v_t &av, const uint4 &b, const fp4_float4_t &c,

@@ -1,4 +1,4 @@
-// tern_gemv_fp4.hip -- decode-path kernel (M <= 4, bf16 activations) whose
+// tern_gemv_fp4.hip -- decode-path kernel (M <= 4, bf16 or 8-bit activations) whose
 // sign-select sums run on the matrix cores with 4-bit weight operands:
 // Y[M,N] = X[M,K] . (T*S)^T.
 //
@@ -7,6 +7,10 @@
 // subtract or skip activations, and the block sum is multiplied by the
 // block's fp16 scale at the block boundary (§1.1, §4.1 third route, §4.2);
 // activations and scales stay on chip (§4.2, §4.3).
+//
+// 8-bit activations are split into two e4m3 terms of scale 1 (tern_fp4.h), so that
+// a block's sum is the exact integer; the block's activation scales (or their row's,
+// read for every block) join the weights' there.
 //
 // Operands (tern_fp4.h): the weights as e2m1 +-2 / 0 (B; 10 VALU operations
 // per 32 weights, about a third of a lane-op per weight against 0.9 for
@@ -93,13 +97,15 @@ constexpr int step_lds() {
     return 8 * M * (F_IMG + 4);
 }
 
-template <int M, bool S8, int Q, int SPW>
-__global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const uint16_t *__restrict__ X,
+// XQ: X holds int8 codes, Rf their scales: that of row m and block g at m xm + g xg.
+template <int M, bool S8, bool XQ, int Q, int SPW>
+__global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *__restrict__ Xv,
                                                                   const uint8_t *__restrict__ P,
                                                                   const uint16_t *__restrict__ S,
                                                                   const int8_t *__restrict__ Qs,
                                                                   const float *__restrict__ Rf, void *__restrict__ Y,
-                                                                  int y_dtype, int N, int K) {
+                                                                  int y_dtype, int N, int K, int xm, int xg) {
+    static_assert(!(S8 && XQ), "one kind of scales beside the weights' fp16 ones");
     constexpr int IMGS = 8 * M;
     constexpr int SL = step_lds<M>();
     constexpr bool ONE = M <= 2;   // hi and lo terms in one MFMA
@@ -130,12 +136,21 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const uint16
     // ---- 1. loads: this lane's activation octets first, then every code and
     //         scale load of the wave (rows past N read zeros; bytes past K
     //         meet zero activations, and their scales are dropped) ----
-    uint4 xq[SPW][M];
+    uint4 xq[SPW][M];      // 8 bf16, or 8 codes in the first two words
+    float xs[SPW][M];
 #pragma unroll
     for (int st = 0; st < SPW; ++st) {
         const int k0 = min((wave * SPW + st) * F_STEP + 8 * lane, K - 8);
 #pragma unroll
-        for (int m = 0; m < M; ++m) xq[st][m] = *reinterpret_cast<const uint4 *>(X + (int64_t)m * K + k0);
+        for (int m = 0; m < M; ++m) {
+            if constexpr (XQ) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(Xv) + (int64_t)m * K + k0);
+                xq[st][m] = make_uint4(v.x, v.y, 0, 0);
+                xs[st][m] = Rf[m * xm + min(4 * (wave * SPW + st) + c, groups - 1) * xg];
+            } else {
+                xq[st][m] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(Xv) + (int64_t)m * K + k0);
+            }
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
     constexpr int SB = S8 ? 1 : 2;
@@ -212,12 +227,16 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const uint16
             uint4 xv = xq[st][m];
             xv.x &= keep;
             xv.y &= keep;
-            xv.z &= keep;
-            xv.w &= keep;
             uint32_t eh, el;   // the 32-run's hi and lo scale exponents
-            split_exponents(quad_max(max_mag8(xv)), eh, el);
             uint32_t he, ho, le, lo;
-            split8(xv, eh, el, he, ho, le, lo);
+            if constexpr (XQ) {
+                split8_codes(xv.x, xv.y, he, ho, le, lo);
+            } else {
+                xv.z &= keep;
+                xv.w &= keep;
+                split_exponents(quad_max(max_mag8(xv)), eh, el);
+                split8(xv, eh, el, he, ho, le, lo);
+            }
             const int ih = (sg * 2 + 0) * M + m;
             const int il = (sg * 2 + 1) * M + m;
             *reinterpret_cast<uint32_t *>(wimg + ih * F_IMG + loff) = he;
@@ -226,8 +245,10 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const uint16
             *reinterpret_cast<uint32_t *>(wimg + il * F_IMG + loff + 8) = lo;
             // one lane of the quad writes the run's scale bytes (the others a
             // spare byte: no branch around the stores)
-            *(so == 0 ? wimg + IMGS * F_IMG + ih * 4 + su : spare_byte) = (char)eh;
-            *(so == 0 ? wimg + IMGS * F_IMG + il * 4 + su : spare_byte) = (char)el;
+            if constexpr (!XQ) {
+                *(so == 0 ? wimg + IMGS * F_IMG + ih * 4 + su : spare_byte) = (char)eh;
+                *(so == 0 ? wimg + IMGS * F_IMG + il * 4 + su : spare_byte) = (char)el;
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -241,7 +262,7 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const uint16
             const uint4 d0 = *reinterpret_cast<const uint4 *>(wimg + img * F_IMG + p * 32);
             const uint4 d1 = *reinterpret_cast<const uint4 *>(wimg + img * F_IMG + p * 32 + 16);
             a[h] = (int8v_t){(int)d0.x, (int)d0.y, (int)d0.z, (int)d0.w, (int)d1.x, (int)d1.y, (int)d1.z, (int)d1.w};
-            sa[h] = (unsigned char)wimg[IMGS * F_IMG + img * 4 + p];
+            sa[h] = XQ ? 127u : (unsigned char)wimg[IMGS * F_IMG + img * 4 + p];
         }
         const bool blk_ok = 4 * s + c < groups;
 #pragma unroll
@@ -253,7 +274,9 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const uint16
             float sc = S8 ? (float)(int32_t)sbits[st][q] : f16_bits_to_float((uint16_t)sbits[st][q]);
             sc = blk_ok ? sc : 0.f;
 #pragma unroll
-            for (int m = 0; m < M; ++m) acc[q][m] = fmaf(sc, ONE ? d[m] + d[2 + m] : d[m], acc[q][m]);
+            for (int m = 0; m < M; ++m)
+                // past K the scales are another block's, and need not be finite
+                acc[q][m] = fmaf(XQ ? (blk_ok ? sc * xs[st][m] : 0.f) : sc, ONE ? d[m] + d[2 + m] : d[m], acc[q][m]);
         }
     }
 #pragma unroll
@@ -377,9 +400,9 @@ F4Shape f4_shape(int64_t M, int64_t N, int64_t K) {
     return g;
 }
 
-template <int M, bool S8, int Q, int SPW>
+template <int M, bool S8, bool XQ, int Q, int SPW>
 hipError_t launch_f4t(const GemmArgs &a, const F4Shape &g) {
-    auto kern = gemv_fp4_kernel<M, S8, Q, SPW>;
+    auto kern = gemv_fp4_kernel<M, S8, XQ, Q, SPW>;
     if (g.lds > 64 * 1024) {
         // raise the dynamic-LDS limit once per device and instantiation (a
         // per-process attribute cache; not a stream operation)
@@ -396,14 +419,15 @@ hipError_t launch_f4t(const GemmArgs &a, const F4Shape &g) {
         }
     }
     hipLaunchKernelGGL(kern, dim3((unsigned)g.grid), dim3(64 * g.nw), g.lds, a.stream,
-                       static_cast<const uint16_t *>(a.X), a.W, a.S, a.Q, a.R, a.Y, a.y_dtype, (int)a.N, (int)a.K);
+                       a.X, a.W, a.S, a.Q, a.R, a.Y, a.y_dtype, (int)a.N, (int)a.K,
+                       a.x_grouped ? (int)(a.K >> 7) : 1, a.x_grouped ? 1 : 0);
     return hipGetLastError();
 }
 
-template <int M, bool S8>
+template <int M, bool S8, bool XQ>
 hipError_t launch_f4s(const GemmArgs &a, const F4Shape &g) {
 #define TERN_F4_CASE(SP, QQ) \
-    if (g.spw == SP && g.q == QQ) return launch_f4t<M, S8, QQ, SP>(a, g);
+    if (g.spw == SP && g.q == QQ) return launch_f4t<M, S8, XQ, QQ, SP>(a, g);
     TERN_F4_TABLE(TERN_F4_CASE)
 #undef TERN_F4_CASE
     return hipErrorInvalidValue;
@@ -411,13 +435,14 @@ hipError_t launch_f4s(const GemmArgs &a, const F4Shape &g) {
 
 template <int M>
 hipError_t launch_f4m(const GemmArgs &a, const F4Shape &g) {
-    return a.Q != nullptr ? launch_f4s<M, true>(a, g) : launch_f4s<M, false>(a, g);
+    if (a.x_dtype == 3) return launch_f4s<M, false, true>(a, g);
+    return a.Q != nullptr ? launch_f4s<M, true, false>(a, g) : launch_f4s<M, false, false>(a, g);
 }
 
 }  // namespace
 
 bool gemv_fp4_fits(int64_t M, int64_t N, int64_t K, int x_dtype) {
-    if (x_dtype != 1 || M < 1 || M > 4 || N < 1 || K < 128) return false;
+    if ((x_dtype != 1 && x_dtype != 3) || M < 1 || M > 4 || N < 1 || K < 128) return false;
     const F4Shape g = f4_shape(M, N, K);
     return g.spw <= F_MAX_SPW && g.q > 0;
 }

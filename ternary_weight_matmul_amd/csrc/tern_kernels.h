@@ -10,7 +10,8 @@ namespace tern {
 
 struct GemmArgs {
     const void *X;       // [M,K] fp16/bf16
-    int x_dtype;         // 0 = fp16, 1 = bf16
+    int x_dtype;         // 0 = fp16, 1 = bf16, 3 = int8 codes with scales R (the decode kernel of up to 4 rows)
+    int x_grouped = 0;   // their scales: [M,K/128] where not 0, else [M]
     const uint8_t *W;    // [N,K/4]
     const uint16_t *S;   // [N,K/128] fp16 bits (when Q is null)
     const int8_t *Q;     // int8 scale codes [N,K/128], or null
@@ -36,8 +37,8 @@ bool gemv_short(int64_t M, int64_t N, int64_t K);
 bool gemv_mfma_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemv_mfma(const GemmArgs &a);
 
-// Decode-path kernel with 4-bit weight operands on the matrix cores (bf16
-// activations split exactly into two e4m3 terms), 1 <= M <= 4.
+// Decode-path kernel with 4-bit weight operands on the matrix cores (bf16 or
+// 8-bit activations split exactly into two e4m3 terms), 1 <= M <= 4.
 bool gemv_fp4_fits(int64_t M, int64_t N, int64_t K, int x_dtype);
 hipError_t launch_gemv_fp4(const GemmArgs &a);
 

@@ -48,6 +48,10 @@ struct Q8Args {
     hipStream_t stream;
 };
 
+// Product for up to 32 rows: waves split K, weights are read once.  fits() is false beyond that and
+// for K < 512.
+bool q8_rows_fits(const Q8Args &a);
+hipError_t launch_q8_rows(const Q8Args &a);
 hipError_t launch_q8_gemm(const Q8Args &a);
 
 }  // namespace tern

@@ -13,6 +13,19 @@ namespace tern {
 typedef int int4v_t __attribute__((ext_vector_type(4)));
 typedef float float4v_t __attribute__((ext_vector_type(4)));
 
+// In both words of x, the fields under MASK change places with those S bits above them.
+template <int S, uint32_t MASK>
+__device__ __forceinline__ void swap_fields(uint64_t &x) {
+    const uint64_t y = x >> S;
+    uint32_t lo = (uint32_t)x, hi = (uint32_t)(x >> 32);
+    const uint32_t t0 = __builtin_amdgcn_bitop3_b32(lo, (uint32_t)y, MASK, (0xF0 ^ 0xCC) & 0xAA);
+    const uint32_t t1 = __builtin_amdgcn_bitop3_b32(hi, (uint32_t)(y >> 32), MASK, (0xF0 ^ 0xCC) & 0xAA);
+    const uint64_t z = (t0 | (uint64_t)t1 << 32) << S;
+    lo = __builtin_amdgcn_bitop3_b32(lo, t0, (uint32_t)z, 0xF0 ^ 0xCC ^ 0xAA);
+    hi = __builtin_amdgcn_bitop3_b32(hi, t1, (uint32_t)(z >> 32), 0xF0 ^ 0xCC ^ 0xAA);
+    x = lo | (uint64_t)hi << 32;
+}
+
 // 32 codes (two words of 16) -> 32 int8 in {-1, 0, +1} in their own order, which is that of the
 // activations' bytes in memory: no byte of those is moved anywhere.
 //
@@ -20,12 +33,9 @@ typedef float float4v_t __attribute__((ext_vector_type(4)));
 // and a mask take one place of all bytes, weights i, 4 + i, 8 + i, 12 + i; so the matrix is
 // transposed first, two swaps of off-diagonal fields (quarters, then within them), after which
 // they are weights 4 i .. 4 i + 3.  A byte permutation then looks each code up in {0, 1, -1, 0}.
-__device__ __forceinline__ void decode32(uint2 code, int4v_t &a, int4v_t &b) {
-    uint64_t x = code.x | (uint64_t)code.y << 32;
-    uint64_t t = (x ^ (x >> 6)) & 0x00CC00CC00CC00CCull;   // field i0 with bit 0 of the byte
-    x ^= t ^ (t << 6);
-    t = (x ^ (x >> 12)) & 0x0000F0F00000F0F0ull;           // and the bits 1
-    x ^= t ^ (t << 12);
+__device__ __forceinline__ void decode32(uint64_t x, int4v_t &a, int4v_t &b) {
+    swap_fields<6, 0x00CC00CCu>(x);    // fields 1 and 3 of the even bytes with 0 and 2 of the odd ones
+    swap_fields<12, 0x0000F0F0u>(x);   // fields 2 and 3 of the lower half with 0 and 1 of the upper one
     constexpr uint32_t VALUES = 0x00FF0100u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

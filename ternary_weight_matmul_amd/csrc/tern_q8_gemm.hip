@@ -135,7 +135,7 @@ __global__ __launch_bounds__(64 * WV, 2) void q8_gemm_kernel(Q8Args a, int tiles
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const int row = wrow0 + 16 * n + li;
-            decode32(*reinterpret_cast<const uint2 *>(b + T::A_LDS + swz<32>(row, p >> 1) + 8 * (p & 1)), w0[n], w1[n]);
+            decode32(*reinterpret_cast<const uint64_t *>(b + T::A_LDS + swz<32>(row, p >> 1) + 8 * (p & 1)), w0[n], w1[n]);
             sc[n] = *reinterpret_cast<const float4v_t *>(b + T::S_AT + (wrow0 + 16 * n + 4 * p) * 4);
         }
         // Activations are read a block of rows ahead, and a block's sums are scaled while the next
