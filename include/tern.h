@@ -349,10 +349,14 @@ tern_status tern_q8_dequant(const int8_t *codes, const float *scales, int32_t q_
  * from -128 to 127 and any scales.  packed_W, scales and group as tern_matmul;
  * x_codes 16-byte, x_scales 4-byte aligned; K <= 2^23.  A NaN or infinite scale
  * reaches its own row or column of Y only.
+ *   workspace: tern_matmul_q8_workspace bytes (TERN_ERR_SHAPE if fewer; none for
+ *       few rows, else 1.5 K for each row of X), 16-byte aligned, for this call
+ *       alone until the stream has passed it.
  */
+size_t tern_matmul_q8_workspace(int64_t M, int64_t N, int64_t K);
 tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t q_group, const uint8_t *packed_W,
                            const uint16_t *scales, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,
-                           int32_t group, hipStream_t stream);
+                           int32_t group, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * tern_moe_route -- the experts of T tokens, and their weights, from a router's

@@ -95,7 +95,9 @@ def _load() -> ctypes.CDLL:
     L.tern_q8_quantize.restype = c_int
     L.tern_q8_dequant.argtypes = [vp, vp, i32, vp, c_int, i64, i64, vp]
     L.tern_q8_dequant.restype = c_int
-    L.tern_matmul_q8.argtypes = [vp, vp, i32, vp, vp, vp, c_int, i64, i64, i64, i32, vp]
+    L.tern_matmul_q8_workspace.argtypes = [i64, i64, i64]
+    L.tern_matmul_q8_workspace.restype = ctypes.c_size_t
+    L.tern_matmul_q8.argtypes = [vp, vp, i32, vp, vp, vp, c_int, i64, i64, i64, i32, vp, ctypes.c_size_t, vp]
     L.tern_matmul_q8.restype = c_int
     L.tern_stream_copy.argtypes = [vp, vp, ctypes.c_uint64, vp]
     L.tern_stream_copy.restype = c_int

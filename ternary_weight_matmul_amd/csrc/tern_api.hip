@@ -219,6 +219,19 @@ tern_status check_q8_pointers(const int8_t *codes, const float *scales) {
     return aligned(scales, 4) ? TERN_OK : TERN_ERR_ALIGN;
 }
 
+bool q8_product_ok(int64_t M, int64_t N, int64_t K) {
+    return M >= 0 && N >= 0 && K >= 0 && M <= kMaxDim && N <= kMaxDim && K <= kQ8MaxK && product_ok(M, N);
+}
+
+// Which kernel takes a product with 8-bit activations: the decode kernel of up to 4 rows, the one for
+// few rows, or tiles, which have a workspace.
+bool q8_decodes(int64_t M, int64_t N, int64_t K) {
+    return M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3);
+}
+size_t q8_workspace(int64_t M, int64_t N, int64_t K) {
+    return q8_decodes(M, N, K) || tern::q8_rows_fits(M, N, K) ? 0 : tern::q8_gemm_workspace(M, N, K);
+}
+
 bool moe_sizes_ok(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {
     if (T < 0 || E < 0 || top_k < 0 || H < 0 || F < 0) return false;
     if (T > kMaxDim || E > kMaxDim || top_k > kMaxDim || H > tern::kMoeMaxWidth || F > tern::kMoeMaxWidth)
@@ -552,11 +565,15 @@ tern_status tern_q8_dequant(const int8_t *codes, const float *scales, int32_t q_
     return from_hip(tern::launch_q8_dequant(codes, scales, Y, dtype_index(y_dtype), M * (K / width), width, stream));
 }
 
+size_t tern_matmul_q8_workspace(int64_t M, int64_t N, int64_t K) {
+    if (!q8_product_ok(M, N, K) || M == 0 || N == 0 || K == 0 || K % TERN_GROUP != 0) return 0;
+    return q8_workspace(M, N, K);
+}
+
 tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t q_group, const uint8_t *packed_W,
                            const uint16_t *scales, void *Y, tern_dtype y_dtype, int64_t M, int64_t N, int64_t K,
-                           int32_t group, hipStream_t stream) {
-    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kQ8MaxK) return TERN_ERR_SHAPE;
-    if (!product_ok(M, N)) return TERN_ERR_SHAPE;
+                           int32_t group, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!q8_product_ok(M, N, K)) return TERN_ERR_SHAPE;
     if (group <= 0 || K % group != 0) return TERN_ERR_GROUP;
     if (!known_dtype(y_dtype)) return TERN_ERR_DTYPE;
     if (group != TERN_GROUP || (q_group != 0 && q_group != TERN_GROUP)) return TERN_ERR_UNSUPPORTED;
@@ -567,7 +584,11 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
     if (x_codes == nullptr || x_scales == nullptr || packed_W == nullptr || scales == nullptr) return TERN_ERR_NULL;
     if (!aligned(x_codes, 16) || !aligned(x_scales, 4) || !aligned(packed_W, 16) || !aligned(scales, 2))
         return TERN_ERR_ALIGN;
-    if (M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3)) {
+    const size_t need = q8_workspace(M, N, K);
+    if (need > 0 && workspace == nullptr) return TERN_ERR_NULL;
+    if (!aligned(workspace, 16)) return TERN_ERR_ALIGN;
+    if (workspace_bytes < need) return TERN_ERR_SHAPE;
+    if (q8_decodes(M, N, K)) {
         tern::GemmArgs g = make_args(x_codes, TERN_BF16, packed_W, scales, nullptr, x_scales, Y, y_dtype, M, N, K, stream);
         g.x_dtype = 3;
         g.x_grouped = q_group != 0;
@@ -584,8 +605,10 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
     a.M = M;
     a.N = N;
     a.K = K;
+    a.terms = workspace;
+    a.w_scales = a.x_scales = nullptr;
     a.stream = stream;
-    return from_hip(tern::q8_rows_fits(a) ? tern::launch_q8_rows(a) : tern::launch_q8_gemm(a));
+    return from_hip(need == 0 ? tern::launch_q8_rows(a) : tern::launch_q8_gemm(a));
 }
 
 }  // extern "C"

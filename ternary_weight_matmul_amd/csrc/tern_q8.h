@@ -45,13 +45,17 @@ struct Q8Args {
     void *Y;             // [M,N]
     int y_dtype;         // 0 = fp16, 1 = bf16, 2 = fp32
     int64_t M, N, K;
+    void *terms;         // workspace of launch_q8_gemm, and what it puts there
+    const float *w_scales, *x_scales;
     hipStream_t stream;
 };
 
 // Product for up to 32 rows: waves split K, weights are read once.  fits() is false beyond that and
 // for K < 512.
-bool q8_rows_fits(const Q8Args &a);
+bool q8_rows_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_q8_rows(const Q8Args &a);
+// Product for many rows, in tiles; the workspace that it needs.
+size_t q8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_q8_gemm(const Q8Args &a);
 
 }  // namespace tern

@@ -247,7 +247,7 @@ hipError_t launch_x(const Q8Args &a) { return a.M > 16 ? launch_m<2, GX>(a) : la
 }  // namespace
 
 // 4 scales are loaded at a time.  Offsets: 32 rows of up to 2^23 bytes.
-bool q8_rows_fits(const Q8Args &a) { return a.M <= 32 && a.K >= 512; }
+bool q8_rows_fits(int64_t M, int64_t, int64_t K) { return M <= 32 && K >= 512; }
 
 hipError_t launch_q8_rows(const Q8Args &a) { return a.grouped ? launch_x<true>(a) : launch_x<false>(a); }
 

@@ -33,4 +33,27 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER) : "memory");
 }
 
+// Loads that go to LDS without the compiler's knowledge.  It waits for those that it knows of where a
+// loop begins anew, for all of them, whatever was asked for last; these are waited for by
+// wait_and_meet alone, which every access to what they write must follow.  They have no registers to
+// write, and `memory` keeps LDS accesses on their sides.  m0 is theirs: the compiler reserves it, and
+// sets it anew for each instruction of its own that reads it.
+typedef int tile_int4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ tile_int4 descriptor(const void *base, int bytes) {   // as buffer_of's
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    return (tile_int4){__builtin_amdgcn_readfirstlane((int)b), __builtin_amdgcn_readfirstlane((int)(b >> 32) & 0xFFFF),
+                       __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+}
+__device__ __forceinline__ uint32_t lds_of(const void *p) {   // a pointer into LDS as the offset there
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+// Lane l's 16 or 4 bytes at off -> LDS offset lds + 16 l or 4 l.
+__device__ __forceinline__ void to_lds16(tile_int4 r, uint32_t lds, int off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+}
+__device__ __forceinline__ void to_lds4(tile_int4 r, uint32_t lds, int off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+}
+
 }  // namespace tern

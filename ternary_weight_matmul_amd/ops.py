@@ -559,8 +559,11 @@ def matmul_q8_into(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tens
     _need_at(packed, "packed", index, _U8, (N, K // 4))
     _need_at(weight_scales, "weight_scales", index, _F16, (N, K // group))
     _need_at(out, "out", index, _FLOATS, (M, N))
+    nbytes = lib.tern_matmul_q8_workspace(M, N, K)
+    ws = codes.new_empty((nbytes,)) if nbytes else None   # as in moe_into
     _launch(lib.tern_matmul_q8, "tern_matmul_q8", codes, codes.data_ptr(), scales.data_ptr(), q_group, packed.data_ptr(),
-            weight_scales.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, group)
+            weight_scales.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, group,
+            ws.data_ptr() if nbytes else 0, nbytes)
     return out
 
 

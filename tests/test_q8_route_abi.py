@@ -54,8 +54,8 @@ def test_a_row_that_is_too_long_for_one_scale():
     assert quant(K=65537) == SHAPE
 
 
-def mm(C=P, XS=P, qg=0, W=P, S=P, Y=P, yd=BF16, M=2, N=16, K=256, G=128):
-    return L.tern_matmul_q8(C, XS, qg, W, S, Y, yd, M, N, K, G, None)
+def mm(C=P, XS=P, qg=0, W=P, S=P, Y=P, yd=BF16, M=2, N=16, K=256, G=128, ws=0, wb=0):
+    return L.tern_matmul_q8(C, XS, qg, W, S, Y, yd, M, N, K, G, ws, wb, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -68,6 +68,17 @@ def mm(C=P, XS=P, qg=0, W=P, S=P, Y=P, yd=BF16, M=2, N=16, K=256, G=128):
 ])
 def test_matmul_q8_rejects(kw, want):
     assert mm(**kw) == want
+
+
+def test_matmul_q8_workspace():
+    assert L.tern_matmul_q8_workspace(4, 16, 256) == 0
+    need = L.tern_matmul_q8_workspace(300, 64, 256)
+    assert need >= 300 * 256 * 3 // 2
+    assert mm(M=300, N=64) == NULL
+    assert mm(M=300, N=64, ws=P, wb=need - 1) == SHAPE
+    assert mm(M=300, N=64, ws=P + 8, wb=need) == ALIGN
+    for bad in ((-1, 4, 128), (300, -4, 128), (300, 64, -128), (300, 64, 100), (0, 64, 128), (300, 0, 128), (300, 64, 0)):
+        assert L.tern_matmul_q8_workspace(*bad) == 0
 
 
 def route(lg=P, ld=F32, b=P, i=P, w=P, T=2, E=64, k=8, sc=1, g=8, kg=4, best=2, rn=1, f=1.0):
