@@ -18,7 +18,7 @@ constexpr int64_t kMaxK = int64_t(1) << 30;
 // of K / 2 bytes).
 constexpr int64_t kMxMaxK = int64_t(1) << 24;
 // Products with 8-bit activations: the same, 128 rows of K bytes.
-constexpr int64_t kQ8MaxK = int64_t(1) << 23;
+constexpr int64_t kQ8MaxK = int64_t(1) << 23, kQ8MaxDim = int64_t(1) << 29;
 constexpr int64_t kMaxProduct = int64_t(1) << 62;
 constexpr size_t kGemvLdsLimit = 152 * 1024;
 
@@ -220,16 +220,27 @@ tern_status check_q8_pointers(const int8_t *codes, const float *scales) {
 }
 
 bool q8_product_ok(int64_t M, int64_t N, int64_t K) {
-    return M >= 0 && N >= 0 && K >= 0 && M <= kMaxDim && N <= kMaxDim && K <= kQ8MaxK && product_ok(M, N);
+    return M >= 0 && N >= 0 && K >= 0 && M <= kQ8MaxDim && N <= kQ8MaxDim && K <= kQ8MaxK && product_ok(M, N);
 }
 
-// Which kernel takes a product with 8-bit activations: the decode kernel of up to 4 rows, the one for
-// few rows, or tiles, which have a workspace.
-bool q8_decodes(int64_t M, int64_t N, int64_t K) {
-    return M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3);
+// Which kernel takes a product with 8-bit activations: the decode kernel of up to 4 rows; the one for
+// few rows, always up to 32 where it reads the weights once; beyond that the one of three with the
+// shortest time by their own estimates.  Measured, in us, few rows / tiles of 64 x 128 / of 128 x 384
+// (estimates in brackets), N x K: 5120 x 5120, 128 rows 15.5 / 27.6 / 62.1 (16 / 28 / 68), 512 rows
+// 51.7 / 39.6 / 65.3 (57 / 41 / 68); 17408 x 5120, 64 rows 36.9 / 28.2 / 66.7 (30 / 28 / 68), 512 rows
+// 182 / 86.9 / 70.7 (223 / 81 / 68); 5120 x 17408, 128 rows 40.9 / 82.1 / 180 (49 / 86 / 188);
+// 1024 x 1024, 1024 rows 7.9 / 9.4 / 25.7 (7 / 8 / 28), 4096 rows 25.6 / 14.3 / 30.5 (21 / 11 / 28).
+enum class Q8Kernel { Decode, Rows, Blocks, Tiles };
+Q8Kernel q8_kernel(int64_t M, int64_t N, int64_t K) {
+    if (M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3)) return Q8Kernel::Decode;
+    const bool rows = tern::q8_rows_fits(M, N, K);
+    if (rows && M <= 32) return Q8Kernel::Rows;
+    const double blocks = tern::q8_blocks_time(M, N, K), tiles = tern::q8_gemm_time(M, N, K);
+    if (rows && tern::q8_rows_time(M, N, K) < (blocks < tiles ? blocks : tiles)) return Q8Kernel::Rows;
+    return blocks < tiles ? Q8Kernel::Blocks : Q8Kernel::Tiles;
 }
 size_t q8_workspace(int64_t M, int64_t N, int64_t K) {
-    return q8_decodes(M, N, K) || tern::q8_rows_fits(M, N, K) ? 0 : tern::q8_gemm_workspace(M, N, K);
+    return q8_kernel(M, N, K) == Q8Kernel::Tiles ? tern::q8_gemm_workspace(M, N, K) : 0;
 }
 
 bool moe_sizes_ok(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t F) {
@@ -584,11 +595,12 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
     if (x_codes == nullptr || x_scales == nullptr || packed_W == nullptr || scales == nullptr) return TERN_ERR_NULL;
     if (!aligned(x_codes, 16) || !aligned(x_scales, 4) || !aligned(packed_W, 16) || !aligned(scales, 2))
         return TERN_ERR_ALIGN;
-    const size_t need = q8_workspace(M, N, K);
+    const Q8Kernel kernel = q8_kernel(M, N, K);
+    const size_t need = kernel == Q8Kernel::Tiles ? tern::q8_gemm_workspace(M, N, K) : 0;
     if (need > 0 && workspace == nullptr) return TERN_ERR_NULL;
     if (!aligned(workspace, 16)) return TERN_ERR_ALIGN;
     if (workspace_bytes < need) return TERN_ERR_SHAPE;
-    if (q8_decodes(M, N, K)) {
+    if (kernel == Q8Kernel::Decode) {
         tern::GemmArgs g = make_args(x_codes, TERN_BF16, packed_W, scales, nullptr, x_scales, Y, y_dtype, M, N, K, stream);
         g.x_dtype = 3;
         g.x_grouped = q_group != 0;
@@ -608,7 +620,9 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
     a.terms = workspace;
     a.w_scales = a.x_scales = nullptr;
     a.stream = stream;
-    return from_hip(need == 0 ? tern::launch_q8_rows(a) : tern::launch_q8_gemm(a));
+    return from_hip(kernel == Q8Kernel::Rows     ? tern::launch_q8_rows(a)
+                    : kernel == Q8Kernel::Blocks ? tern::launch_q8_blocks(a)
+                                                 : tern::launch_q8_gemm(a));
 }
 
 }  // extern "C"

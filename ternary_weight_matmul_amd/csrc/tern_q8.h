@@ -50,12 +50,17 @@ struct Q8Args {
     hipStream_t stream;
 };
 
-// Product for up to 32 rows: waves split K, weights are read once.  fits() is false beyond that and
-// for K < 512.
+// Products.  Few rows: waves split K, and each 32 rows read the weights.
 bool q8_rows_fits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_q8_rows(const Q8Args &a);
-// Product for many rows, in tiles; the workspace that it needs.
+// Tiles of 64 x 128 outputs.
+hipError_t launch_q8_blocks(const Q8Args &a);
+// Tiles of 128 x 384; the workspace that they need.
 size_t q8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_q8_gemm(const Q8Args &a);
+// What each takes, about, in us.
+double q8_rows_time(int64_t M, int64_t N, int64_t K);
+double q8_blocks_time(int64_t M, int64_t N, int64_t K);
+double q8_gemm_time(int64_t M, int64_t N, int64_t K);
 
 }  // namespace tern

@@ -399,6 +399,11 @@ size_t scales_bytes(int64_t rows, int64_t K) { return (size_t)((rows + S_ROWS - 
 
 size_t q8_gemm_workspace(int64_t M, int64_t N, int64_t K) { return terms_bytes(M, K) + scales_bytes(N, K) + scales_bytes(M, K); }
 
+double q8_gemm_time(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = ((M + 127) / 128) * ((N + 383) / 384);
+    return 18 + (double)(K / 128) * (1.75 * (double)((tiles + 255) / 256) - 0.5);
+}
+
 hipError_t launch_q8_gemm(const Q8Args &a0) {
     Q8Args a = a0;
     char *ws = static_cast<char *>(a.terms);

@@ -1,10 +1,10 @@
-// tern_q8_rows.hip -- Y[M,N] = X . (T*S)^T for up to 32 rows, with X in 8 bits with
-// scales and ternary weights.
+// tern_q8_rows.hip -- Y[M,N] = X . (T*S)^T for few rows, with X in 8 bits with scales
+// and ternary weights.
 //
-// Mathematics as in tern_q8_gemm.hip: a block of 128's sum is an exact integer from
+// Mathematics as in tern_q8_blocks.hip: a block of 128's sum is an exact integer from
 // v_mfma_i32_16x16x64_i8, its scales are applied in fp32.
 //
-// Work layout.  A workgroup owns 16 RW weight rows over all of K.  Its waves are KW
+// Work layout.  A workgroup owns 16 RW weight rows over all of K, for 32 rows of X.  Its waves are KW
 // groups of RW: a group takes every KW-th step of 512 weights, and a wave of it 16
 // weight rows.  A wave's codes, 128 bytes a row, go to registers as whole lines, 8
 // rows an instruction, the first TT turns' at the start: a line that comes from HBM
@@ -43,6 +43,7 @@ __device__ __forceinline__ void wave_order() {
 }
 
 constexpr int min(int a, int b) { return a < b ? a : b; }
+constexpr int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // What every lane holds, in a scalar register: a buffer descriptor made from anything else is
 // gathered lane by lane in a loop around each load.
@@ -71,11 +72,13 @@ __global__ __launch_bounds__(64 * RW * KW) void q8_rows_kernel(Q8Args a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), kw = wave / RW, rw = wave % RW;
     const int p = lane >> 4, li = lane & 15;
-    const int M = (int)a.M, N = (int)a.N, K = (int)a.K, groups = K >> 7, steps = (K + 511) >> 9, wrow = K >> 2;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int M = uniform((int)min64(a.M - m0, 16 * MT)), N = (int)a.N, K = (int)a.K;   // M: of this workgroup
+    const int groups = K >> 7, steps = (K + 511) >> 9, wrow = K >> 2;
     const int n0 = (blockIdx.x * RW + rw) * 16;
     const int first = uniform(min(n0, N)), rows = uniform(min(N - min(n0, N), 16));   // a minimum is a vector instruction
-    const __amdgpu_buffer_rsrc_t rx = buffer_of(a.Q, M * K);
-    const __amdgpu_buffer_rsrc_t rxs = buffer_of(a.XS, GX ? M * groups * 4 : 0);
+    const __amdgpu_buffer_rsrc_t rx = buffer_of(a.Q + m0 * K, M * K);
+    const __amdgpu_buffer_rsrc_t rxs = buffer_of(a.XS + (GX ? m0 * groups : 0), GX ? M * groups * 4 : 0);
     const __amdgpu_buffer_rsrc_t rc = buffer_of(a.W + (int64_t)first * wrow, rows * wrow);
     const uint16_t *srow = a.S + (int64_t)min(n0 + li, N - 1) * groups;
 
@@ -197,8 +200,8 @@ __global__ __launch_bounds__(64 * RW * KW) void q8_rows_kernel(Q8Args a) {
         for (int v = 0; v < 4; ++v) {
             const int m = 16 * (t % MT) + 4 * (l >> 4) + v;
             if (m >= M) continue;
-            const float r = GX ? y[v] : y[v] * a.XS[m];
-            const int64_t at = (int64_t)m * N + n;
+            const float r = GX ? y[v] : y[v] * a.XS[m0 + m];
+            const int64_t at = (m0 + m) * N + n;
             if (a.y_dtype == 2) store_out<2>(a.Y, at, r);
             else if (a.y_dtype == 1) store_out<1>(a.Y, at, r);
             else store_out<0>(a.Y, at, r);
@@ -206,25 +209,31 @@ __global__ __launch_bounds__(64 * RW * KW) void q8_rows_kernel(Q8Args a) {
     }
 }
 
+int64_t chunks(int64_t M) { return M <= 16 ? 1 : (M + 31) / 32; }   // of the rows of X
+
 template <int RW, int KW, int MT, int TT, bool GX>
 hipError_t launch_t(const Q8Args &a) {
     const unsigned grid = (unsigned)((a.N + 16 * RW - 1) / (16 * RW));
-    hipLaunchKernelGGL((q8_rows_kernel<RW, KW, MT, TT, GX>), dim3(grid), dim3(64 * RW * KW), 0, a.stream, a);
+    hipLaunchKernelGGL((q8_rows_kernel<RW, KW, MT, TT, GX>), dim3(grid, (unsigned)chunks(a.M)), dim3(64 * RW * KW), 0,
+                       a.stream, a);
     return hipGetLastError();
 }
 
 // Weight rows of a workgroup, in sixteens: the busiest CU takes ceil(workgroups / CUs) of them, plus
 // about one sixteen's worth of work that every workgroup has.  Measured at M = 16, K = 5120, in us, for
 // 1, 2, 3, 4, 5 sixteens: 5120 rows 11.4, 7.8, 9.2, 9.7, 11.6; 17408 rows 27.2, 16.9, 18.0, 16.0, 12.8.
-int sixteens(int64_t N) {
-    const int64_t blocks = (N + 15) / 16;
-    int64_t best = 0;
-    int r = 1;
+struct Split {
+    int sixteens;
+    int64_t cost;
+};
+Split split(int64_t M, int64_t N) {
+    const int64_t blocks = (N + 15) / 16, times = chunks(M);
+    Split best = {1, 0};
     for (int i = 1; i <= 5; ++i) {
-        const int64_t cost = ((blocks + i - 1) / i + 255) / 256 * (i + 1);
-        if (i == 1 || cost < best) best = cost, r = i;
+        const int64_t cost = ((blocks + i - 1) / i * times + 255) / 256 * (i + 1);
+        if (i == 1 || cost < best.cost) best = {i, cost};
     }
-    return r;
+    return best;
 }
 
 // Groups that split K: 8 to 10 waves a workgroup (more of them take longer to start than they save:
@@ -232,7 +241,7 @@ int sixteens(int64_t N) {
 // turns ahead pay with long K (17408: 16.4 us against 16.9 with 2), not with 3 turns (8.0 against 7.8).
 template <int MT, bool GX>
 hipError_t launch_m(const Q8Args &a) {
-    switch (sixteens(a.N)) {
+    switch (split(a.M, a.N).sixteens) {
     case 1: return launch_t<1, MT == 1 ? 5 : 4, MT, 2, GX>(a);
     case 2: return a.K > 12288 ? launch_t<2, 4, MT, 4, GX>(a) : launch_t<2, 4, MT, 2, GX>(a);
     case 3: return launch_t<3, 3, MT, 2, GX>(a);
@@ -246,8 +255,10 @@ hipError_t launch_x(const Q8Args &a) { return a.M > 16 ? launch_m<2, GX>(a) : la
 
 }  // namespace
 
-// 4 scales are loaded at a time.  Offsets: 32 rows of up to 2^23 bytes.
-bool q8_rows_fits(int64_t M, int64_t, int64_t K) { return M <= 32 && K >= 512; }
+// 4 scales are loaded at a time, and a grid has 65535 chunks.  Offsets: 32 rows of up to 2^23 bytes.
+bool q8_rows_fits(int64_t M, int64_t, int64_t K) { return K >= 512 && chunks(M) <= 65535; }
+
+double q8_rows_time(int64_t M, int64_t N, int64_t K) { return 2 + 0.23 * (double)split(M, N).cost * (double)((K + 511) / 512); }
 
 hipError_t launch_q8_rows(const Q8Args &a) { return a.grouped ? launch_x<true>(a) : launch_x<false>(a); }
 

@@ -184,3 +184,72 @@ def test_a_graph_and_another_stream(M):
         g2.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, tern.matmul_q8(*d)) and torch.equal(y2, tern.matmul_q8(*d, out_dtype=torch.float32))
+
+
+# Large products have a kernel of their own, with a workspace.
+LARGE = (1100, 7501, 2816)
+
+
+@pytest.mark.parametrize("group,yd,odd", [(0, "bf16", 1), (128, "f32", 1), (128, "f16", 0), (0, "f32", 0)])
+def test_large_product(group, yd, odd):
+    M, N, K = LARGE
+    N -= 1 - odd
+    print(f"matmul_q8 M={M} N={N} K={K} group={group} -> {yd}", flush=True)
+    q, xs, packed, ws = problem(M, N, K, group, M + group, lo=-128)
+    want, bound = R.product(q, xs, packed, ws, DT[yd])
+    R.assert_close(run(q, xs, packed, ws, yd), want, bound, "matmul_q8")
+
+
+def test_large_product_exact_and_every_place_of_a_weight():
+    """Power-of-two scales and one weight a row, at every k."""
+    M, N, K = LARGE
+    rng = np.random.default_rng(1)
+    q = rng.integers(-128, 128, (M, K)).astype(np.int8)
+    q[3] = -128
+    t = np.zeros((N, K), dtype=np.int64)
+    t[np.arange(N), np.arange(N) % K] = np.where(np.arange(N) % 3 == 0, -1, 1)
+    t[-2], t[-1] = 1, -1
+    xs = np.exp2(rng.integers(-2, 3, (M, K // 128))).astype(np.float32)
+    ws = np.exp2(rng.integers(-3, 2, (N, K // 128))).astype(np.float16)
+    packed = R.pack_ternary(t)
+    want, _ = R.product(q, xs, packed, ws, torch.float32)
+    assert np.array_equal(R.f64(run(q, xs, packed, ws, "f32")), want)
+
+
+def test_large_product_infinities_and_nans_stay_in_their_row_and_column():
+    M, N, K = LARGE
+    q, xs, packed, ws = problem(M, N, K, 128, 9)
+    clean = R.f64(run(q, xs, packed, ws, "f32"))
+    xs[M // 2, -1] = np.nan
+    ws[17, 2] = np.inf
+    ws[N - 1, 4] = np.nan
+    y = R.f64(run(q, xs, packed, ws, "f32"))
+    rows, cols = np.arange(M) != M // 2, ~np.isin(np.arange(N), (17, N - 1))
+    assert np.isnan(y[M // 2]).all() and np.isnan(y[:, N - 1]).all() and not np.isfinite(y[:, 17]).any()
+    assert np.array_equal(y[np.ix_(rows, cols)], clean[np.ix_(rows, cols)])
+
+
+def test_large_products_in_two_graphs_and_on_two_streams():
+    M, N, K = LARGE
+    p = [[dev(a) for a in problem(M, N, K, 0, seed)] for seed in (1, 2)]
+    want = [tern.matmul_q8(*d) for d in p]
+    sides = [torch.cuda.Stream() for _ in p]
+    torch.cuda.synchronize()
+    got = []
+    for d, side in zip(p, sides):
+        with torch.cuda.stream(side):
+            got.append([tern.matmul_q8(*d) for _ in range(3)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for ys, w in zip(got, want) for y in ys)
+    graphs = [torch.cuda.CUDAGraph() for _ in p]
+    out = []
+    for d, g in zip(p, graphs):
+        with torch.cuda.graph(g):
+            out.append(tern.matmul_q8(*d))
+    for _ in range(3):
+        for y in out:
+            y.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(out, want))
