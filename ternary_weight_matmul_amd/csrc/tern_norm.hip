@@ -29,6 +29,7 @@
 
 #include "tern_device.h"
 #include "tern_q8.h"
+#include "tern_tile.h"
 
 namespace tern {
 
@@ -49,44 +50,44 @@ struct Elem<2> {
     typedef float type;
 };
 
-// 8 consecutive elements at any address that their type allows, `n` of them (the rest is `fill`).
+// 8 consecutive elements at any address that their type allows.
 template <typename E>
-__device__ __forceinline__ void load8_of(const E *at, int n, float fill, float (&v)[8]) {
-    if (n >= 8) {
-        E e[8];
-        __builtin_memcpy(e, at, sizeof(e));
+__device__ __forceinline__ void load8_of(const E *at, float (&v)[8]) {
+    E e[8];
+    __builtin_memcpy(e, at, sizeof(e));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)at[i] : fill;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
 }
 
 template <typename E>
-__device__ __forceinline__ void store8_of(E *at, int n, const float (&v)[8]) {
-    if (n >= 8) {
-        E e[8];
+__device__ __forceinline__ void store8_of(E *at, const float (&v)[8]) {
+    E e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = (E)v[i];
-        __builtin_memcpy(at, e, sizeof(e));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) at[i] = (E)v[i];
-    }
+    for (int i = 0; i < 8; ++i) e[i] = (E)v[i];
+    __builtin_memcpy(at, e, sizeof(e));
 }
 
-__device__ __forceinline__ void load8_any(const void *at, int dtype, int64_t i, int n, float fill, float (&v)[8]) {
-    if (dtype == 2) load8_of(static_cast<const float *>(at) + i, n, fill, v);
-    else if (dtype == 1) load8_of(static_cast<const __bf16 *>(at) + i, n, fill, v);
-    else load8_of(static_cast<const _Float16 *>(at) + i, n, fill, v);
+__device__ __forceinline__ void load8_any(const void *at, int dtype, int64_t i, float (&v)[8]) {
+    if (dtype == 2) load8_of(static_cast<const float *>(at) + i, v);
+    else if (dtype == 1) load8_of(static_cast<const __bf16 *>(at) + i, v);
+    else load8_of(static_cast<const _Float16 *>(at) + i, v);
 }
 
-__device__ __forceinline__ void store8_any(void *at, int dtype, int64_t i, int n, const float (&v)[8]) {
-    if (dtype == 2) store8_of(static_cast<float *>(at) + i, n, v);
-    else if (dtype == 1) store8_of(static_cast<__bf16 *>(at) + i, n, v);
-    else store8_of(static_cast<_Float16 *>(at) + i, n, v);
+__device__ __forceinline__ void store8_any(void *at, int dtype, int64_t i, const float (&v)[8]) {
+    if (dtype == 2) store8_of(static_cast<float *>(at) + i, v);
+    else if (dtype == 1) store8_of(static_cast<__bf16 *>(at) + i, v);
+    else store8_of(static_cast<_Float16 *>(at) + i, v);
+}
+
+__device__ __forceinline__ float load_any(const void *at, int dtype, int64_t i) {
+    if (dtype == 2) return static_cast<const float *>(at)[i];
+    return dtype == 1 ? (float)static_cast<const __bf16 *>(at)[i] : (float)static_cast<const _Float16 *>(at)[i];
+}
+
+__device__ __forceinline__ void store_any(void *at, int dtype, int64_t i, float v) {
+    if (dtype == 2) static_cast<float *>(at)[i] = v;
+    else if (dtype == 1) static_cast<__bf16 *>(at)[i] = (__bf16)v;
+    else static_cast<_Float16 *>(at)[i] = (_Float16)v;
 }
 
 template <int CTRL>
@@ -120,24 +121,34 @@ __device__ __forceinline__ double lane_of(double v, int l) {
     return __builtin_bit_cast(double, (uint64_t)lane_of((uint32_t)b, l) | (uint64_t)lane_of((uint32_t)(b >> 32), l) << 32);
 }
 
-// The codes of 8 values h w, whose neighbours' largest magnitude is a, a byte each.
+// 1 / sqrt(x) in 64 bits: the instruction's estimate, good to 2^-24, and a Newton step.  x = 0 and
+// infinity have no step.
+__device__ __forceinline__ double inverse_root(double x) {
+    const double y = __builtin_amdgcn_rsq(x), z = y * __builtin_fma(-0.5 * x * y, y, 1.5);
+    return z == z ? z : y;
+}
+
+// The codes of 8 values h w, whose neighbours' largest magnitude is a, a byte each.  127 h w / a plus
+// 1.5 2^23 has the nearest integer in its low bits.
 __device__ __forceinline__ uint64_t codes_of(const float (&h)[8], const float (&w)[8], float a) {
-    const float inv = 127.f / a;
-    bool sure = a >= 0x1p-100f;   // 127 / a fits an fp32
-    int n[8];
+    const float about = __builtin_amdgcn_rcpf(a), inv = 127.f * fmaf(fmaf(-a, about, 1.f), about, about);
+    float u[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = h[i] * w[i] * inv, r = __builtin_rintf(t);
-        sure = sure && __builtin_fabsf(t - r) < 0.5f - 0x1p-15f;
-        n[i] = (int)r;
+        const float p = h[i] * w[i];
+        u[i] = fmaf(p, inv, 0x1.8p23f);
+        off = fmaxf(off, __builtin_fabsf(fmaf(p, inv, -(u[i] - 0x1.8p23f))));
     }
-    if (!sure) {
+    uint32_t n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = __builtin_bit_cast(uint32_t, u[i]);
+    if (!(off < 0.5f - 0x1p-15f && a >= 0x1p-100f && a <= 0x1p100f)) {   // beyond, 1 / a leaves fp32
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
             float hi = h[0], wi = w[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) hi = i == j ? h[j] : hi, wi = i == j ? w[j] : wi;
-            const int c = (int)__builtin_rint(127.0 * ((double)hi * (double)wi) / (double)a);
+            const uint32_t c = (uint32_t)(int)__builtin_rint(127.0 * ((double)hi * (double)wi) / (double)a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) n[j] = i == j ? c : n[j];
         }
@@ -150,10 +161,35 @@ __device__ __forceinline__ uint64_t codes_of(const float (&h)[8], const float (&
     return b[0] | (uint64_t)b[1] << 32;
 }
 
-// XT: type of X; RT: of the residual, -1 without one.
+// f = f1 f2, f1 a power of two.
+struct Factor {
+    double f;
+    float f1, f2;
+};
+__device__ __forceinline__ Factor factor_of(double sum, double per, double eps, bool normalize) {
+    const double f = normalize ? inverse_root(__builtin_fma(sum, per, eps)) : 1.0;
+    const int e = min(max((int)(__builtin_bit_cast(uint64_t, f) >> 52 & 0x7FF) - 1023, -126), 127);
+    return {f, __builtin_bit_cast(float, (uint32_t)(e + 127) << 23),
+            (float)(f * __builtin_bit_cast(double, (uint64_t)(1023 - e) << 52))};
+}
+
+// The scale of a block whose largest magnitude has these bits: 0 for a block of zeros, NaN for one
+// with an infinity or a NaN; the codes are 0 in both.
+__device__ __forceinline__ bool has_codes(uint32_t bits) { return bits - 1 < 0x7F7FFFFFu; }
+__device__ __forceinline__ float scale_of(uint32_t bits, double f) {
+    if (has_codes(bits)) return (float)((double)__builtin_bit_cast(float, bits) * f * (1.0 / 127.0));
+    return bits != 0 ? __builtin_nanf("") : f == f ? 0.f : (float)f;
+}
+
+// XT: type of X; RT: of the residual, -1 without one.  8 <= K <= 8 NV TPR.
+// The last of a row's eights begins at K - 8 and shares values with the one before it: every load is
+// whole.  What is shared counts once in the sum, and is written twice alike.
 template <int XT, int RT, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
     constexpr int NT = TPR < 256 ? 256 : TPR, ROWS = NT / TPR, WAVES = NT / 64;
+    // Weights stay in registers, and the next row is asked for while this one is worked on, where there
+    // are registers for them.
+    constexpr bool HELD = NV <= 5, AHEAD = NV <= 3;
     typedef typename Elem<XT>::type X;
     typedef typename Elem<(RT < 0 ? 0 : RT)>::type R;
     __shared__ double sums[2][WAVES];
@@ -162,50 +198,70 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = (int)a.K;
     const bool grouped = a.grouped != 0, coded = a.Q != nullptr;
-    // Read twice, by then from the L1: held in registers they cost as many as the row itself.
-    auto weights = [&](int k, float (&w)[8]) __attribute__((always_inline)) {
+    auto first = [&](int v) __attribute__((always_inline)) { return min((v * TPR + t) * 8, K - 8); };
+    struct Eights {
+        X x[8];
+        R r[8];
+    };
+    auto ask = [&](Eights (&e)[NV], int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) __builtin_memcpy(e[v].x, static_cast<const X *>(a.X) + row * K + first(v), sizeof(e[v].x));
+        if constexpr (RT >= 0) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) __builtin_memcpy(e[v].r, static_cast<const R *>(a.R) + row * K + first(v), sizeof(e[v].r));
+        }
+    };
+    auto weights = [&](int v, float (&w)[8]) __attribute__((always_inline)) {
         if (a.W != nullptr) {
-            load8_any(a.W, a.w_dtype, k, K - k, 1.f, w);
+            load8_any(a.W, a.w_dtype, first(v), w);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = 1.f;
         }
     };
-    int slot = 0;
     // every thread of a workgroup takes part in each turn: rows past the last one are read as row M - 1
     // and not written
-    for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.M; row0 += (int64_t)gridDim.x * ROWS) {
+    auto mine = [&](int64_t row0) __attribute__((always_inline)) { return min(row0 + tid / TPR, a.M - 1); };
+    const double per = 1.0 / K;
+    int64_t row0 = (int64_t)blockIdx.x * ROWS;
+    Eights e[NV];
+    ask(e, mine(row0));
+    float held[HELD ? NV : 1][8];
+    if constexpr (HELD) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) weights(v, held[v]);
+    }
+    int slot = 0;
+    for (;;) {
         const bool there = row0 + tid / TPR < a.M;
-        const int64_t row = there ? row0 + tid / TPR : a.M - 1, at = row * K;
+        const int64_t row = mine(row0), at = row * K;
+        row0 += (int64_t)gridDim.x * ROWS;
         float h[NV][8];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int k = (v * TPR + t) * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[v][i] = 0.f;
-            if (k < K) load8_of(static_cast<const X *>(a.X) + at + k, K - k, 0.f, h[v]);
+            for (int i = 0; i < 8; ++i) {
+                h[v][i] = (float)e[v].x[i];
+                if constexpr (RT >= 0) h[v][i] = (float)(R)(h[v][i] + (float)e[v].r[i]);
+            }
         }
-        if constexpr (RT >= 0) {
-            float r[NV][8];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int k = (v * TPR + t) * 8;
-                if (k < K) load8_of(static_cast<const R *>(a.R) + at + k, K - k, 0.f, r[v]);
-            }
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int k = (v * TPR + t) * 8;
-                if (k >= K) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[v][i] = (float)(R)(h[v][i] + r[v][i]);
-                if (there) store8_of(static_cast<R *>(a.H) + at + k, K - k, h[v]);
-            }
+        if constexpr (AHEAD) {
+            if (row0 < a.M) ask(e, mine(row0));
         }
         double sum = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            const int twice = (v * TPR + t) * 8 - first(v);
+            double s = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)h[v][i], (double)h[v][i], sum);
+            for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[v][i], (double)h[v][i], s);
+            if (twice > 0) {
+                s = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i >= twice) s = __builtin_fma((double)h[v][i], (double)h[v][i], s);
+            }
+            sum += s;
         }
         sum = row_sum(sum);
         // magnitudes as integers: their order is that of the values, NaN above infinity
@@ -215,14 +271,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
         if (coded) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int k = (v * TPR + t) * 8;
-                float w[8];
-                if (k < K) {
-                    weights(k, w);
+                float again[8];
+                if constexpr (!HELD) weights(v, again);
+                const float(&w)[8] = HELD ? held[HELD ? v : 0] : again;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        top[v] = max(top[v], __builtin_bit_cast(uint32_t, h[v][i] * w[i]) & 0x7FFFFFFFu);
-                }
+                for (int i = 0; i < 8; ++i)
+                    top[v] = max(top[v], __builtin_bit_cast(uint32_t, h[v][i] * w[i]) & 0x7FFFFFFFu);
             }
             if (grouped) {   // 128 values are 16 lanes' 8
 #pragma unroll
@@ -244,7 +298,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
                 sums[slot][wave] = sum;
                 if (!grouped) tops[slot][wave] = top[0];
             }
-            __syncthreads();
+            wait_and_meet<63>();   // not for loads and stores
             sum = 0;
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) sum += sums[slot][i];
@@ -254,41 +308,63 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
             }
             slot ^= 1;
         }
-        // f = f1 f2, f1 a power of two
-        double f = 1.0;
-        if (a.normalize) f = 1.0 / __builtin_sqrt(sum / K + (double)a.eps);
-        const int e = min(max((int)(__builtin_bit_cast(uint64_t, f) >> 52 & 0x7FF) - 1023, -126), 127);
-        const float f1 = __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
-        const float f2 = (float)(f / (double)f1);
-        if (!there) continue;
+        const Factor f = factor_of(sum, per, (double)a.eps, a.normalize != 0);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int k = (v * TPR + t) * 8;
-            if (k >= K) continue;
-            float w[8];
-            weights(k, w);
+            const int k = first(v);
+            if (!there || (v * TPR + t) * 8 >= K) continue;
+            // all of the row has been read by now: H may be R
+            if constexpr (RT >= 0) store8_of(static_cast<R *>(a.H) + at + k, h[v]);
+            float again[8];
+            if constexpr (!HELD) weights(v, again);
+            const float(&w)[8] = HELD ? held[HELD ? v : 0] : again;
             if (a.Y != nullptr) {
                 float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = h[v][i] * f1 * f2 * w[i];
-                store8_any(a.Y, a.y_dtype, at + k, K - k, y);
+                for (int i = 0; i < 8; ++i) y[i] = h[v][i] * f.f1 * f.f2 * w[i];
+                store8_any(a.Y, a.y_dtype, at + k, y);
             }
             if (coded) {
                 const uint32_t bits = grouped ? top[v] : top[0];
-                // 0 for a block of zeros, NaN for one with an infinity or a NaN; the codes are 0 in both
-                const float most = __builtin_bit_cast(float, bits);
-                const bool some = bits - 1 < 0x7F7FFFFFu;
-                float scale = (float)((double)most * f / 127.0);
-                if (!some) scale = bits != 0 ? __builtin_nanf("") : f == f ? 0.f : (float)f;
-                const uint64_t q = some ? codes_of(h[v], w, most) : 0;
-                int8_t *qp = a.Q + at + k;
-                if (K - k >= 8) {
-                    __builtin_memcpy(qp, &q, 8);
-                } else {
-                    for (int i = 0; i < K - k; ++i) qp[i] = (int8_t)(q >> (8 * i));
-                }
-                if (grouped ? k % 128 == 0 : k == 0) a.S[grouped ? (at + k) / 128 : row] = scale;
+                const uint64_t q = has_codes(bits) ? codes_of(h[v], w, __builtin_bit_cast(float, bits)) : 0;
+                __builtin_memcpy(a.Q + at + k, &q, 8);
+                if (t % 16 == 0 && (grouped || v * TPR + t == 0)) a.S[grouped ? (at + k) / 128 : row] = scale_of(bits, f.f);
             }
+        }
+        if (row0 >= a.M) break;
+        if constexpr (!AHEAD) ask(e, mine(row0));
+    }
+}
+
+// Rows of fewer than 8 values, one to a thread.
+__global__ __launch_bounds__(256) void norm_short_kernel(NormArgs a) {
+    const int K = (int)a.K;
+    for (int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x; row < a.M; row += (int64_t)gridDim.x * 256) {
+        const int64_t at = row * K;
+        float h[8], w[8];
+        double sum = 0;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = min(i, K - 1);
+            h[i] = i < K ? load_any(a.X, a.x_dtype, at + k) : 0.f;
+            if (a.R != nullptr && i < K) {
+                h[i] = h[i] + load_any(a.R, a.r_dtype, at + k);
+                store_any(a.H, a.r_dtype, at + k, h[i]);
+                h[i] = load_any(a.H, a.r_dtype, at + k);
+            }
+            w[i] = a.W != nullptr ? load_any(a.W, a.w_dtype, k) : 1.f;
+            sum = __builtin_fma((double)h[i], (double)h[i], sum);
+            if (i < K) top = max(top, __builtin_bit_cast(uint32_t, h[i] * w[i]) & 0x7FFFFFFFu);
+        }
+        const Factor f = factor_of(sum, 1.0 / K, (double)a.eps, a.normalize != 0);
+        const uint64_t q = a.Q != nullptr && has_codes(top) ? codes_of(h, w, __builtin_bit_cast(float, top)) : 0;
+        if (a.Q != nullptr) a.S[row] = scale_of(top, f.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= K) continue;
+            if (a.Y != nullptr) store_any(a.Y, a.y_dtype, at + i, h[i] * f.f1 * f.f2 * w[i]);
+            if (a.Q != nullptr) a.Q[at + i] = (int8_t)(q >> (8 * i));
         }
     }
 }
@@ -325,11 +401,15 @@ __global__ __launch_bounds__(256) void q8_dequant_kernel(const int8_t *__restric
         const float s = S[row];
         const int64_t at = row * K;
         for (int k = (blockIdx.y * lanes + t) * 8; k < K; k += gridDim.y * lanes * 8) {
-            float q[8];
-            load8_of(Q + at + k, K - k, 0.f, q);
+            if (K - k >= 8) {
+                float q[8];
+                load8_of(Q + at + k, q);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] *= s;
-            store8_of(static_cast<E *>(Y) + at + k, K - k, q);
+                for (int i = 0; i < 8; ++i) q[i] *= s;
+                store8_of(static_cast<E *>(Y) + at + k, q);
+            } else {
+                for (int i = k; i < K; ++i) static_cast<E *>(Y)[at + i] = (E)((float)Q[at + i] * s);
+            }
         }
     }
 }
@@ -338,6 +418,10 @@ __global__ __launch_bounds__(256) void q8_dequant_kernel(const int8_t *__restric
 
 // The residual has X's type or is fp32.
 hipError_t launch_norm(const NormArgs &a) {
+    if (a.K < 8) {
+        hipLaunchKernelGGL(norm_short_kernel, dim3((unsigned)std::min<int64_t>((a.M + 255) / 256, 4096)), dim3(256), 0, a.stream, a);
+        return hipGetLastError();
+    }
     if (a.R == nullptr) {
         if (a.x_dtype == 0) return launch_row<0, -1>(a);
         return a.x_dtype == 1 ? launch_row<1, -1>(a) : launch_row<2, -1>(a);
