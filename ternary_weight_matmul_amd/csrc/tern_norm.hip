@@ -13,16 +13,19 @@
 // change the code, one value in 16000, it is formed anew in 64 bits, in which the
 // quotient of these numbers is rounded to the right side of any border.
 //
-// Squares are summed in 64 bits: no row of any of the types leaves the range, and
-// two conversions and additions an element hide behind the loads.  f is applied as
-// a power of two and the rest, so that it need not fit an fp32.
+// Squares are summed in 64 bits: no row of any of the types leaves the range.  f is
+// applied as a power of two and the rest, so that it need not fit an fp32.
 //
-// Work layout.  TPR threads hold a row in registers, NV times 8 consecutive values
-// each, so that everything is read once and written once; a workgroup takes rows
-// in turn and keeps its weights.  Rows of up to 2048 values are a wave's or a part
-// of one and need no barrier, longer ones one each.
+// Work layout.  A row stays in the registers of its threads, NV times 8 consecutive
+// values each, so that everything is read once and written once; a workgroup takes
+// rows in turn, keeps its weights, and asks for the next row while it works on one.
+// Rows of up to 1024 values are a wave's or a part of one and need no barrier,
+// longer ones one each.
 //
-// Bound: HBM.
+// Bound: HBM where there are thousands of rows (2048 x 5120 with a residual stream
+// 18.3 us, 4.6 TB/s, a copy of as much 19.1), else the way of the first row's lines
+// from memory, and with 8-bit outputs the vector instructions, 15 a value
+// (333 x 17408 20.8 us, 3.1 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -181,34 +184,39 @@ __device__ __forceinline__ float scale_of(uint32_t bits, double f) {
     return bits != 0 ? __builtin_nanf("") : f == f ? 0.f : (float)f;
 }
 
-// XT: type of X; RT: of the residual, -1 without one.  8 <= K <= 8 NV TPR.
+// XT: type of X; RT: of the residual, -1 without one.  TPR: threads of a row, 16 or 64 of a workgroup
+// of 256, or 0: the workgroup's, up to MOST.  8 <= K <= 8 NV threads.
 // The last of a row's eights begins at K - 8 and shares values with the one before it: every load is
 // whole.  What is shared counts once in the sum, and is written twice alike.
-template <int XT, int RT, int TPR, int NV>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
-    constexpr int NT = TPR < 256 ? 256 : TPR, ROWS = NT / TPR, WAVES = NT / 64;
+template <int XT, int RT, int TPR, int NV, int MOST>
+__global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
+    constexpr int ROWS = TPR > 0 ? MOST / TPR : 1;
     // Weights stay in registers, and the next row is asked for while this one is worked on, where there
     // are registers for them.
-    constexpr bool HELD = NV <= 5, AHEAD = NV <= 3;
+    constexpr bool HELD = NV <= 4, AHEAD = NV <= 3;
+    constexpr int TOGETHER = NV < 4 ? NV : 4;   // eights that are asked for at once
     typedef typename Elem<XT>::type X;
     typedef typename Elem<(RT < 0 ? 0 : RT)>::type R;
-    __shared__ double sums[2][WAVES];
-    __shared__ uint32_t tops[2][WAVES];
-    const int tid = threadIdx.x, t = tid % TPR, lane = tid & 63;
+    __shared__ double sums[2][16];
+    __shared__ uint32_t tops[2][16];
+    const int tid = threadIdx.x, threads = TPR > 0 ? TPR : blockDim.x, t = TPR > 0 ? tid % threads : tid, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int my_row = TPR > 0 ? tid / threads : 0;
     const int K = (int)a.K;
     const bool grouped = a.grouped != 0, coded = a.Q != nullptr;
-    auto first = [&](int v) __attribute__((always_inline)) { return min((v * TPR + t) * 8, K - 8); };
+    auto first = [&](int v) __attribute__((always_inline)) { return min((v * threads + t) * 8, K - 8); };
     struct Eights {
         X x[8];
         R r[8];
     };
-    auto ask = [&](Eights (&e)[NV], int64_t row) __attribute__((always_inline)) {
+    auto ask = [&](Eights (&e)[TOGETHER], int64_t row, int v0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) __builtin_memcpy(e[v].x, static_cast<const X *>(a.X) + row * K + first(v), sizeof(e[v].x));
+        for (int v = 0; v < TOGETHER; ++v)
+            __builtin_memcpy(e[v].x, static_cast<const X *>(a.X) + row * K + first(v0 + v), sizeof(e[v].x));
         if constexpr (RT >= 0) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) __builtin_memcpy(e[v].r, static_cast<const R *>(a.R) + row * K + first(v), sizeof(e[v].r));
+            for (int v = 0; v < TOGETHER; ++v)
+                __builtin_memcpy(e[v].r, static_cast<const R *>(a.R) + row * K + first(v0 + v), sizeof(e[v].r));
         }
     };
     auto weights = [&](int v, float (&w)[8]) __attribute__((always_inline)) {
@@ -221,11 +229,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     };
     // every thread of a workgroup takes part in each turn: rows past the last one are read as row M - 1
     // and not written
-    auto mine = [&](int64_t row0) __attribute__((always_inline)) { return min(row0 + tid / TPR, a.M - 1); };
+    auto mine = [&](int64_t row0) __attribute__((always_inline)) { return min(row0 + my_row, a.M - 1); };
     const double per = 1.0 / K;
     int64_t row0 = (int64_t)blockIdx.x * ROWS;
-    Eights e[NV];
-    ask(e, mine(row0));
+    Eights e[TOGETHER];
+    ask(e, mine(row0), 0);
     float held[HELD ? NV : 1][8];
     if constexpr (HELD) {
 #pragma unroll
@@ -233,25 +241,29 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     }
     int slot = 0;
     for (;;) {
-        const bool there = row0 + tid / TPR < a.M;
+        const bool there = row0 + my_row < a.M;
         const int64_t row = mine(row0), at = row * K;
         row0 += (int64_t)gridDim.x * ROWS;
         float h[NV][8];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            if (v > 0 && v % TOGETHER == 0) {
+                __builtin_amdgcn_sched_barrier(0);   // not before: there are no registers
+                ask(e, row, v);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[v][i] = (float)e[v].x[i];
-                if constexpr (RT >= 0) h[v][i] = (float)(R)(h[v][i] + (float)e[v].r[i]);
+                h[v][i] = (float)e[v % TOGETHER].x[i];
+                if constexpr (RT >= 0) h[v][i] = (float)(R)(h[v][i] + (float)e[v % TOGETHER].r[i]);
             }
         }
         if constexpr (AHEAD) {
-            if (row0 < a.M) ask(e, mine(row0));
+            if (row0 < a.M) ask(e, mine(row0), 0);
         }
         double sum = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int twice = (v * TPR + t) * 8 - first(v);
+            const int twice = (v * threads + t) * 8 - first(v);
             double s = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) s = __builtin_fma((double)h[v][i], (double)h[v][i], s);
@@ -287,32 +299,29 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
                 top[0] = row_max(top[0]);
             }
         }
-        if constexpr (TPR >= 64) {
+        if constexpr (TPR != 16) {
             sum = (lane_of(sum, 0) + lane_of(sum, 16)) + (lane_of(sum, 32) + lane_of(sum, 48));
             if (!grouped)
                 top[0] = max(max(lane_of(top[0], 0), lane_of(top[0], 16)), max(lane_of(top[0], 32), lane_of(top[0], 48)));
         }
-        if constexpr (TPR > 64) {
+        if constexpr (TPR == 0) {
             // two slots in turn: a wave writes one again only after a barrier that follows its last read
             if (lane == 0) {
                 sums[slot][wave] = sum;
                 if (!grouped) tops[slot][wave] = top[0];
             }
             wait_and_meet<63>();   // not for loads and stores
-            sum = 0;
-#pragma unroll
-            for (int i = 0; i < WAVES; ++i) sum += sums[slot][i];
-            if (!grouped) {
-#pragma unroll
-                for (int i = 0; i < WAVES; ++i) top[0] = max(top[0], tops[slot][i]);
-            }
+            // 16 lanes take the waves'
+            const int i = lane & 15, waves = threads >> 6;
+            sum = row_sum(i < waves ? sums[slot][i] : 0.0);
+            if (!grouped) top[0] = row_max(i < waves ? tops[slot][i] : 0u);
             slot ^= 1;
         }
         const Factor f = factor_of(sum, per, (double)a.eps, a.normalize != 0);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int k = first(v);
-            if (!there || (v * TPR + t) * 8 >= K) continue;
+            if (!there || (v * threads + t) * 8 >= K) continue;
             // all of the row has been read by now: H may be R
             if constexpr (RT >= 0) store8_of(static_cast<R *>(a.H) + at + k, h[v]);
             float again[8];
@@ -328,11 +337,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
                 const uint32_t bits = grouped ? top[v] : top[0];
                 const uint64_t q = has_codes(bits) ? codes_of(h[v], w, __builtin_bit_cast(float, bits)) : 0;
                 __builtin_memcpy(a.Q + at + k, &q, 8);
-                if (t % 16 == 0 && (grouped || v * TPR + t == 0)) a.S[grouped ? (at + k) / 128 : row] = scale_of(bits, f.f);
+                if (t % 16 == 0 && (grouped || v * threads + t == 0)) a.S[grouped ? (at + k) / 128 : row] = scale_of(bits, f.f);
             }
         }
         if (row0 >= a.M) break;
-        if constexpr (!AHEAD) ask(e, mine(row0));
+        if constexpr (!AHEAD) ask(e, mine(row0), 0);
     }
 }
 
@@ -369,27 +378,36 @@ __global__ __launch_bounds__(256) void norm_short_kernel(NormArgs a) {
     }
 }
 
-template <int XT, int RT, int TPR, int NV>
+template <int XT, int RT, int TPR, int NV, int MOST>
 hipError_t launch_t(const NormArgs &a) {
-    constexpr int NT = TPR < 256 ? 256 : TPR, ROWS = NT / TPR;
-    // enough workgroups to fill every CU, each with rows left to take in turn
-    const int64_t need = (a.M + ROWS - 1) / ROWS, most = 256 * (2048 / NT);
-    hipLaunchKernelGGL((norm_kernel<XT, RT, TPR, NV>), dim3((unsigned)std::min(need, most)), dim3(NT), 0, a.stream, a);
+    const int threads = TPR > 0 ? MOST : (int)((a.K + 512 * NV - 1) / (512 * NV)) * 64;
+    constexpr int ROWS = TPR > 0 ? MOST / TPR : 1;
+    // Up to 16 waves a CU, in as many workgroups as give the busiest CU the fewest rows: 2048 x 5120 with
+    // a residual took 18.3 us, against 22.3 with up to 20 waves, and 20.9 with the most workgroups of 16
+    // waves that there is room for.
+    const int64_t need = (a.M + ROWS - 1) / ROWS;
+    int64_t grid = 0, least = 0;
+    for (int64_t c = std::max(16 * 64 / threads, 1); c >= 1; --c) {
+        const int64_t rows = (need + 256 * c - 1) / (256 * c) * c;
+        if (grid == 0 || rows < least) least = rows, grid = 256 * c;
+    }
+    grid = std::min(grid, need);
+    hipLaunchKernelGGL((norm_kernel<XT, RT, TPR, NV, MOST>), dim3((unsigned)grid), dim3(threads), 0, a.stream, a);
     return hipGetLastError();
 }
 
+// Two eights a thread up to 8192, which leaves room for many waves (three: 2048 x 8192 29.7 us against
+// 25.4, 2048 x 5119 24.5 against 21.8, 4096 x 6144 without a residual 19.9 against 22.6), then as few as
+// the workgroup's threads allow.
 template <int XT, int RT>
 hipError_t launch_row(const NormArgs &a) {
-    if (a.K <= 128) return launch_t<XT, RT, 16, 1>(a);
-    if (a.K <= 512) return launch_t<XT, RT, 64, 1>(a);
-    if (a.K <= 1024) return launch_t<XT, RT, 64, 2>(a);
-    if (a.K <= 2048) return launch_t<XT, RT, 256, 1>(a);
-    if (a.K <= 4096) return launch_t<XT, RT, 256, 2>(a);
-    if (a.K <= 6144) return launch_t<XT, RT, 256, 3>(a);
-    if (a.K <= 12288) return launch_t<XT, RT, 512, 3>(a);
-    if (a.K <= 20480) return launch_t<XT, RT, 512, 5>(a);
-    if (a.K <= 32768) return launch_t<XT, RT, 1024, 4>(a);
-    return launch_t<XT, RT, 1024, 8>(a);
+    if (a.K <= 128) return launch_t<XT, RT, 16, 1, 256>(a);
+    if (a.K <= 512) return launch_t<XT, RT, 64, 1, 256>(a);
+    if (a.K <= 1024) return launch_t<XT, RT, 64, 2, 256>(a);
+    if (a.K <= 8192) return launch_t<XT, RT, 0, 2, 512>(a);
+    if (a.K <= 12288) return launch_t<XT, RT, 0, 3, 512>(a);
+    if (a.K <= 32768) return launch_t<XT, RT, 0, 4, 1024>(a);
+    return launch_t<XT, RT, 0, 8, 1024>(a);
 }
 
 template <int YT>
