@@ -30,7 +30,14 @@
 // weights its columns: a lane holds 16 rows of one column and needs one weight scale.
 // A tile's sums are scaled while the next one's matrix instructions run.
 //
-// Bound: the matrix cores, and what feeds them from LDS.
+// Bound: the issue of 2 waves a SIMD.  A wave's step has 24 matrix and 161 vector
+// instructions, 96 of which scale its sums, of 32 and 4 cycles: 1.5 and 1.3 thousand
+// cycles for both waves, of 2.0 GHz under this load, against 3.0 measured; loads
+// alone take 0.6 us a step, products alone 0.7, both 1.4.  2048 x 5120 -> 17408: 212
+// us, 1.7 * 10^15 operations a second, 12 of them for the first kernel (222 with 193
+// vector instructions: offsets of loads counted up in vector registers, halves of
+// operands moved together, codes decoded in 64-bit shifts).  Reading operands half a
+// step ahead of their use, and decoding between the products, changed nothing.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -88,11 +95,9 @@ __device__ __forceinline__ void pack6(const uint32_t (&c)[8], uint32_t *r) {
 }
 
 // One wave for 32 rows and one block.
-__global__ __launch_bounds__(256) void q8_terms_kernel(const int8_t *__restrict__ Q, char *__restrict__ out, int M,
-                                                       int groups, int64_t units) {
-    const int lane = threadIdx.x & 63, h = lane >> 5, i = lane & 31;
-    const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (u >= units) return;
+// Terms of 32 rows' block u, by one wave.
+__device__ __forceinline__ void split_terms(const int8_t *Q, char *out, int M, int groups, int64_t u, int lane) {
+    const int h = lane >> 5, i = lane & 31;
     const int64_t row = u / groups * T_ROWS + i;
     const int g = (int)(u % groups);
     uint32_t r[24];
@@ -138,13 +143,24 @@ __device__ __forceinline__ void turn_scales(const void *S, float *out, int rows,
     }
 }
 
-__global__ __launch_bounds__(256) void q8_scales_kernel(const uint16_t *__restrict__ S, const float *__restrict__ XS,
-                                                        float *__restrict__ out, float *__restrict__ xout, int N, int M,
-                                                        int groups, int64_t w_units, int64_t units) {
+// Waves: the terms' blocks, then the weights' and the activations' scales.
+__global__ __launch_bounds__(256) void q8_layout_kernel(const int8_t *__restrict__ Q, const uint16_t *__restrict__ S,
+                                                        const float *__restrict__ XS, char *__restrict__ terms,
+                                                        float *__restrict__ w_scales, float *__restrict__ x_scales, int M,
+                                                        int N, int groups, int64_t t_units, int64_t w_units, int64_t units) {
     const int lane = threadIdx.x & 63;
     const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (u < w_units) turn_scales<false>(S, out, N, groups, u, lane);
-    else if (u < units) turn_scales<true>(XS, xout, M, groups, u - w_units, lane);
+    if (u < t_units) split_terms(Q, terms, M, groups, u, lane);
+    else if (u < t_units + w_units) turn_scales<false>(S, w_scales, N, groups, u - t_units, lane);
+    else if (u < units) turn_scales<true>(XS, x_scales, M, groups, u - t_units - w_units, lane);
+}
+
+// 16 codes a word -> their +-2 / 0 as 4-bit floats, the odd ones in the second word of each pair: sign
+// and nonzero bit, 5 instructions.
+__device__ __forceinline__ uint4 weights_of(uint32_t a, uint32_t b) {
+    const uint32_t u = __builtin_amdgcn_bitop3_b32(a, a >> 1, 0x55555555u, 0xF0 ^ (0xCC & 0xAA));
+    const uint32_t v = __builtin_amdgcn_bitop3_b32(b, b >> 1, 0x55555555u, 0xF0 ^ (0xCC & 0xAA));
+    return make_uint4((u << 2) & 0xCCCCCCCCu, u & 0xCCCCCCCCu, (v << 2) & 0xCCCCCCCCu, v & 0xCCCCCCCCu);
 }
 
 template <int WM, int WN, int MB, int NB, int ST, bool GX>
@@ -202,11 +218,16 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_ker
     const int wrow = K >> 2, wrows = min(T::BN, N - n0);
     const int xband = groups * T_BLOCK;   // bytes of 32 rows' terms
     const int sblock = wave % T::SB, xblock = wave % T::XB, sband = groups * S_ROWS * 4;
-    const int4v_t rx = descriptor(static_cast<const char *>(a.terms) + (int64_t)(m0 / T_ROWS) * xband, T::BM / T_ROWS * xband);
-    const int4v_t rw = descriptor(a.W + (int64_t)n0 * wrow, wrows * wrow);
-    const int4v_t rs = descriptor(a.w_scales + (int64_t)min(n0 / S_ROWS + sblock, (N - 1) / S_ROWS) * (groups * S_ROWS), sband);
-    const int4v_t rxs = descriptor(GX ? a.x_scales + (int64_t)min(m0 / S_ROWS + xblock, (M - 1) / S_ROWS) * (groups * S_ROWS) : nullptr,
-                                   GX ? sband : 0);
+    const char *const rx = static_cast<const char *>(a.terms) + (int64_t)(m0 / T_ROWS) * xband;
+    const uint8_t *const rw = a.W + (int64_t)n0 * wrow;
+    const float *const rs = a.w_scales + (int64_t)min(n0 / S_ROWS + sblock, (N - 1) / S_ROWS) * (groups * S_ROWS);
+    const float *const rxs = GX ? a.x_scales + (int64_t)min(m0 / S_ROWS + xblock, (M - 1) / S_ROWS) * (groups * S_ROWS) : nullptr;
+    // What step s reads of `bytes` from base: the step moves the descriptor, in scalar registers, and
+    // the offsets of a lane stay as they are.  Rows past the end are out of range as before; steps past
+    // it have nothing in range.
+    auto of_step = [&](const void *base, int s, int each, int bytes) TERN_INLINE {
+        return descriptor(static_cast<const char *>(base) + (int64_t)s * each, s < groups ? bytes : 0);
+    };
 
     // 16 bytes a lane, 1 KB an instruction: a sixth of 32 rows' terms, or 64 bytes, two steps, of 16 rows
     // of codes (32 bytes of 32 rows took twice as long as as many terms); 4 bytes a lane of scales, which
@@ -224,16 +245,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_ker
         woff[i] = row * wrow + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
     }
     auto fetch_terms = [&](uint32_t to, int s, int i) TERN_INLINE {   // and scales, load i of LOADS
-        const bool there = s < groups;
         if (i < T::XI)
-            to_lds16(rx, to + (wave * T::XI + i) * 1024, there ? xoff[i < T::XI ? i : 0] + s * T_BLOCK : OUT_OF_RANGE);
+            to_lds16(of_step(rx, s, T_BLOCK, T::BM / T_ROWS * xband), to + (wave * T::XI + i) * 1024, xoff[i < T::XI ? i : 0]);
         else if (i == T::XI)
-            to_lds4(rs, to + T::S_AT + sblock * 256, there ? s * 256 + lane * 4 : OUT_OF_RANGE);
+            to_lds4(of_step(rs, s, S_ROWS * 4, sband), to + T::S_AT + sblock * 256, lane * 4);
         else
-            to_lds4(rxs, to + T::X_AT + xblock * 256, there ? s * 256 + lane * 4 : OUT_OF_RANGE);
+            to_lds4(of_step(rxs, s, S_ROWS * 4, sband), to + T::X_AT + xblock * 256, lane * 4);
     };
     auto fetch_codes = [&](uint32_t to, int s, int i) TERN_INLINE {   // of steps s and s + 1
-        to_lds16(rw, to + (wave * T::WI + i) * 1024, s < groups ? woff[i] + s * 32 : OUT_OF_RANGE);
+        to_lds16(of_step(rw, s, 32, wrows * wrow), to + (wave * T::WI + i) * 1024, woff[i]);
     };
 
     float16v_t acc[MB][NB];
@@ -261,8 +281,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_ker
         for (int n = 0; n < NB; ++n) {
             const int row = (wn * NB + n) * 32 + li;
             const int4v_t c = *reinterpret_cast<const int4v_t *>(cb + row * 64 + (((2 * (decltype(i)::value & 1) + h) ^ ((row >> 2) & 3)) << 4));
-            w[n][0] = fp4_weights((uint32_t)c[0], (uint32_t)c[1]);
-            w[n][1] = fp4_weights((uint32_t)c[2], (uint32_t)c[3]);
+            w[n][0] = weights_of((uint32_t)c[0], (uint32_t)c[1]);
+            w[n][1] = weights_of((uint32_t)c[2], (uint32_t)c[3]);
             sc[n] = *reinterpret_cast<const float *>(b + T::S_AT + row * 4);
         }
         float16v_t d[2];
@@ -282,7 +302,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_ker
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 x[c] = *reinterpret_cast<const int4v_t *>(xb + c * 1024 + lane * 16);
-                y[c] = *reinterpret_cast<const int2v_t *>(xb + 4096 + c * 512 + lane * 8);
+                // volatile: two of them read at once would have to be moved behind their x
+                y[c] = *(const volatile __attribute__((address_space(3))) int2v_t *)(xb + 4096 + c * 512 + lane * 8);
             }
             if constexpr (GX) {
 #pragma unroll
@@ -412,15 +433,12 @@ hipError_t launch_q8_gemm(const Q8Args &a0) {
     a.w_scales = w_scales;
     a.x_scales = x_scales;
     const int groups = (int)(a.K / 128);
-    const int64_t units = (a.M + T_PAD - 1) / T_PAD * (T_PAD / T_ROWS) * groups;
-    hipLaunchKernelGGL(q8_terms_kernel, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, a.stream, a.Q, ws, (int)a.M, groups, units);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t pieces = (groups + 7) / 8, wu = (a.N + S_ROWS - 1) / S_ROWS * pieces;
-    const int64_t su = wu + (a.grouped ? (a.M + S_ROWS - 1) / S_ROWS * pieces : 0);
-    hipLaunchKernelGGL(q8_scales_kernel, dim3((unsigned)((su + 3) / 4)), dim3(256), 0, a.stream, a.S, a.XS, w_scales, x_scales,
-                       (int)a.N, (int)a.M, groups, wu, su);
-    e = hipGetLastError();
+    const int64_t tu = (a.M + T_PAD - 1) / T_PAD * (T_PAD / T_ROWS) * groups, pieces = (groups + 7) / 8;
+    const int64_t wu = (a.N + S_ROWS - 1) / S_ROWS * pieces;
+    const int64_t units = tu + wu + (a.grouped ? (a.M + S_ROWS - 1) / S_ROWS * pieces : 0);
+    hipLaunchKernelGGL(q8_layout_kernel, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, a.stream, a.Q, a.S, a.XS, ws, w_scales,
+                       x_scales, (int)a.M, (int)a.N, groups, tu, wu, units);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return a.grouped ? launch_x<true>(a) : launch_x<false>(a);
 }

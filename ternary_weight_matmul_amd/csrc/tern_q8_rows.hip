@@ -20,9 +20,10 @@
 // Loads with nothing to fetch have offsets out of range and return zeros.
 // Finally the groups' partial tiles meet in LDS and are summed in a fixed order.
 //
-// Bound: the decoding of the codes, some 200 vector instructions a wave and step
-// (4.5 us of 12.8 at 16 x 5120 -> 17408), and what cannot overlap it: the launch, the
-// first lines' way from HBM, and the CUs that N / 16 RW workgroups leave idle.
+// Bound: the lines' way from HBM and the decoding of the codes, some 200 vector
+// instructions a wave and step, which overlap only in part.  16 rows, 5120 -> 5120,
+// 5120 -> 17408 and 17408 -> 5120: 7.9, 13.2 and 16.6 us; the loads alone 6.5, 9.9 and
+// 12.9, the codes' alone 5.4, 8.8 and 9.7, of which 2 are the launch.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

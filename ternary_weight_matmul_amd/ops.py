@@ -474,8 +474,6 @@ def rms_norm_into(x: torch.Tensor, weight: Optional[torch.Tensor], out: Optional
     M, K = x.shape
     if out is None and codes is None:
         raise ValueError("out or codes must be given")
-    if weight is not None:
-        _need_at(weight, "weight", index, _FLOATS, (K,))
     if out is not None:
         _need_at(out, "out", index, _FLOATS, (M, K))
     group = 0
@@ -487,11 +485,19 @@ def rms_norm_into(x: torch.Tensor, weight: Optional[torch.Tensor], out: Optional
     elif scales is not None:
         raise ValueError("codes must be given with scales")
     if residual is not None:
-        _need_at(residual, "residual", index, (x.dtype, torch.float32), (M, K))
         residual_out = residual if residual_out is None else residual_out
         _need_at(residual_out, "residual_out", index, (residual.dtype,), (M, K))
     elif residual_out is not None:
         raise ValueError("residual must be given with residual_out")
+    _rms_norm(x, index, M, K, weight, out, codes, scales, group, eps, residual, residual_out)
+
+
+def _rms_norm(x, index, M, K, weight, out, codes, scales, group, eps, residual, residual_out) -> None:
+    """The launch, of inputs yet to be checked (x aside) and outputs that are as they should be."""
+    if weight is not None:
+        _need_at(weight, "weight", index, _FLOATS, (K,))
+    if residual is not None:
+        _need_at(residual, "residual", index, (x.dtype, torch.float32), (M, K))
     _launch(lib.tern_rms_norm, "tern_rms_norm", x, x.data_ptr(), _TORCH_CODE[x.dtype],
             residual.data_ptr() if residual is not None else 0, _TORCH_CODE[residual.dtype] if residual is not None else 0,
             weight.data_ptr() if weight is not None else 0, _TORCH_CODE[weight.dtype] if weight is not None else 0,
@@ -504,9 +510,13 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
              residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None):
     """y = h / sqrt(mean(h^2) + eps) * weight of every row, h = x [M,K]; y in x's type unless out_dtype is
     given.  With a residual [M,K] h is x + residual in the residual's type, and (y, h) is returned."""
-    out = x.new_empty(x.shape, dtype=out_dtype)
-    h = torch.empty_like(residual) if residual is not None else None
-    rms_norm_into(x, weight, out=out, eps=eps, residual=residual, residual_out=h)
+    index = _need_matrix(x, "x", _FLOATS)
+    M, K = x.shape
+    if out_dtype is not None and out_dtype not in _FLOATS:
+        raise TypeError("out_dtype must be float32, bfloat16 or float16")
+    out = x.new_empty((M, K), dtype=out_dtype)
+    h = None if residual is None else x.new_empty((M, K), dtype=residual.dtype)
+    _rms_norm(x, index, M, K, weight, out, None, None, 0, eps, residual, h)
     return out if h is None else (out, h)
 
 
@@ -514,11 +524,12 @@ def rms_norm_q8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e
                 residual: Optional[torch.Tensor] = None, group: int = 0):
     """rms_norm with the outputs as 8-bit activations: (codes int8 [M,K], scales fp32 [M,1], or [M,K/128]
     with group 128), and h with a residual."""
-    _need_matrix(x, "x", _FLOATS)
-    codes = x.new_empty(x.shape, dtype=torch.int8)
-    scales = x.new_empty(_q_shape(*x.shape, group), dtype=torch.float32)
-    h = torch.empty_like(residual) if residual is not None else None
-    rms_norm_into(x, weight, codes=codes, scales=scales, eps=eps, residual=residual, residual_out=h)
+    index = _need_matrix(x, "x", _FLOATS)
+    M, K = x.shape
+    codes = x.new_empty((M, K), dtype=torch.int8)
+    scales = x.new_empty(_q_shape(M, K, group), dtype=torch.float32)
+    h = None if residual is None else x.new_empty((M, K), dtype=residual.dtype)
+    _rms_norm(x, index, M, K, weight, None, codes, scales, group, eps, residual, h)
     return (codes, scales) if h is None else (codes, scales, h)
 
 
