@@ -17,8 +17,9 @@ constexpr int64_t kMaxK = int64_t(1) << 30;
 // Products with microscaled weights: offsets inside the rows of one workgroup are 32-bit (72 rows
 // of K / 2 bytes).
 constexpr int64_t kMxMaxK = int64_t(1) << 24;
-// Products with 8-bit activations: the same, 128 rows of K bytes.
-constexpr int64_t kQ8MaxK = int64_t(1) << 23, kQ8MaxDim = int64_t(1) << 29;
+// Products with 8-bit activations: the same, 128 rows of K bytes; a grid has fewer than 2^32 threads,
+// and that of few rows up to 8 for each row of W.
+constexpr int64_t kQ8MaxK = int64_t(1) << 23, kQ8MaxDim = int64_t(1) << 28;
 constexpr int64_t kMaxProduct = int64_t(1) << 62;
 constexpr size_t kGemvLdsLimit = 152 * 1024;
 
@@ -235,6 +236,7 @@ Q8Kernel q8_kernel(int64_t M, int64_t N, int64_t K) {
     if (M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3)) return Q8Kernel::Decode;
     const bool rows = tern::q8_rows_fits(M, N, K);
     if (rows && M <= 32) return Q8Kernel::Rows;
+    if (M <= 32) return Q8Kernel::Blocks;   // no workspace for so few
     const double blocks = tern::q8_blocks_time(M, N, K), tiles = tern::q8_gemm_time(M, N, K);
     if (rows && tern::q8_rows_time(M, N, K) < (blocks < tiles ? blocks : tiles)) return Q8Kernel::Rows;
     return blocks < tiles ? Q8Kernel::Blocks : Q8Kernel::Tiles;

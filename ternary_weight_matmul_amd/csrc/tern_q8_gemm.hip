@@ -223,10 +223,11 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_ker
     const float *const rs = a.w_scales + (int64_t)min(n0 / S_ROWS + sblock, (N - 1) / S_ROWS) * (groups * S_ROWS);
     const float *const rxs = GX ? a.x_scales + (int64_t)min(m0 / S_ROWS + xblock, (M - 1) / S_ROWS) * (groups * S_ROWS) : nullptr;
     // What step s reads of `bytes` from base: the step moves the descriptor, in scalar registers, and
-    // the offsets of a lane stay as they are.  Rows past the end are out of range as before; steps past
-    // it have nothing in range.
+    // the offsets of a lane stay as they are.  Its range ends where the bytes end: rows past the last one
+    // are out of it, and so is the second step of a last pair that has none; steps past the end have
+    // nothing in range.
     auto of_step = [&](const void *base, int s, int each, int bytes) TERN_INLINE {
-        return descriptor(static_cast<const char *>(base) + (int64_t)s * each, s < groups ? bytes : 0);
+        return descriptor(static_cast<const char *>(base) + (int64_t)s * each, s < groups ? bytes - s * each : 0);
     };
 
     // 16 bytes a lane, 1 KB an instruction: a sixth of 32 rows' terms, or 64 bytes, two steps, of 16 rows

@@ -562,6 +562,12 @@ def matmul_q8_into(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tens
     [N,K/group]."""
     index = codes.get_device()
     M, K, q_group = _need_q8(codes, scales, index)
+    _need_at(out, "out", index, _FLOATS, (M, packed.shape[0]))
+    return _matmul_q8(codes, scales, packed, weight_scales, out, index, M, K, q_group, group)
+
+
+def _matmul_q8(codes, scales, packed, weight_scales, out, index, M, K, q_group, group) -> torch.Tensor:
+    """The launch, of weights yet to be checked."""
     if group <= 0:
         raise ValueError("group must be positive")
     if packed.dim() != 2 or packed.shape[1] * 4 != K:
@@ -569,8 +575,7 @@ def matmul_q8_into(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tens
     N = packed.shape[0]
     _need_at(packed, "packed", index, _U8, (N, K // 4))
     _need_at(weight_scales, "weight_scales", index, _F16, (N, K // group))
-    _need_at(out, "out", index, _FLOATS, (M, N))
-    nbytes = lib.tern_matmul_q8_workspace(M, N, K)
+    nbytes = lib.tern_matmul_q8_workspace(M, N, K) if M > 32 else 0
     ws = codes.new_empty((nbytes,)) if nbytes else None   # as in moe_into
     _launch(lib.tern_matmul_q8, "tern_matmul_q8", codes, codes.data_ptr(), scales.data_ptr(), q_group, packed.data_ptr(),
             weight_scales.data_ptr(), out.data_ptr(), _TORCH_CODE[out.dtype], M, N, K, group,
@@ -581,8 +586,12 @@ def matmul_q8_into(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tens
 def matmul_q8(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tensor, weight_scales: torch.Tensor,
               out_dtype: torch.dtype = torch.bfloat16, group: int = 128) -> torch.Tensor:
     """Y[M,N] = X . (T*S)^T with X held as 8-bit activations (from rms_norm_q8 or q8_quantize); a new tensor."""
-    out = codes.new_empty((codes.shape[0], packed.shape[0]), dtype=out_dtype)
-    return matmul_q8_into(codes, scales, packed, weight_scales, out, group)
+    index = codes.get_device()
+    M, K, q_group = _need_q8(codes, scales, index)
+    if out_dtype not in _FLOATS:
+        raise TypeError("out_dtype must be float32, bfloat16 or float16")
+    out = codes.new_empty((M, packed.shape[0]), dtype=out_dtype)
+    return _matmul_q8(codes, scales, packed, weight_scales, out, index, M, K, q_group, group)
 
 
 # --- one GPU's share of a sharded layer (no communication here) -------------

@@ -191,9 +191,12 @@ LARGE = (1100, 7501, 2816)
 
 
 @pytest.mark.parametrize("group,yd,odd", [(0, "bf16", 1), (128, "f32", 1), (128, "f16", 0), (0, "f32", 0)])
-def test_large_product(group, yd, odd):
+@pytest.mark.parametrize("more", [0, 128])   # an even and an odd number of blocks: codes come for two at a time
+def test_large_product(group, yd, odd, more):
     M, N, K = LARGE
     N -= 1 - odd
+    K += more
+    assert tern.lib.tern_matmul_q8_workspace(M, N, K) > 0
     print(f"matmul_q8 M={M} N={N} K={K} group={group} -> {yd}", flush=True)
     q, xs, packed, ws = problem(M, N, K, group, M + group, lo=-128)
     want, bound = R.product(q, xs, packed, ws, DT[yd])
