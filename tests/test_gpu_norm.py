@@ -246,3 +246,28 @@ def test_a_graph_and_another_stream():
         torch.cuda.synchronize()
         want, y = tern.rms_norm_q8(x, w, residual=r, group=128), tern.rms_norm(x, w)
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(got_y, y)
+
+
+@pytest.mark.parametrize("M,K", [(7000, 130), (4100, 1030), (2055, 1500), (1300, 5119), (700, 9000), (530, 12800), (300, 33000)])
+@pytest.mark.parametrize("xd,rd", [("bf16", "bf16"), ("f16", "f32")])
+def test_rows_in_turns(M, K, xd, rd):
+    """More rows than workgroups, which take the next one while they write the last; the stream in place."""
+    print(f"norm M={M} K={K} {xd} {rd} in place", flush=True)
+    x, r = values((M, K), xd, M + K), (values((M, K), rd, M) * 4).to(DT[rd])
+    w = (values((1, K), "f32", K, 0)[0] * 0.3 + 1).to(DT[xd])
+    group = 0 if K % 128 else 128
+    codes, scales, h = tern.rms_norm_q8(x.to(DEV), w.to(DEV), residual=r.to(DEV), group=group)
+    rd_, y = r.to(DEV), torch.empty((M, K), dtype=DT[xd], device=DEV)
+    c2, s2 = torch.empty_like(codes), torch.empty_like(scales)
+    tern.rms_norm_into(x.to(DEV), w.to(DEV), out=y, codes=c2, scales=s2, residual=rd_)
+    assert torch.equal(rd_, h) and torch.equal(c2, codes) and torch.equal(s2, scales)
+    wh, wy, v, f = R.norm(x, w, 1e-6, r)
+    assert np.array_equal(R.f64(h), wh)
+    R.assert_close(y, wy, R.norm_bound(wy, DT[xd]), "norm")
+    q, ws = R.quantize(v, f, group)
+    assert np.array_equal(codes.cpu().numpy(), q)
+    equal_scales(scales.cpu(), ws)
+    if xd == rd:   # the sum into x's own buffer
+        x2 = x.to(DEV)
+        tern.rms_norm_into(x2, w.to(DEV), out=y, residual=r.to(DEV), residual_out=x2)
+        assert torch.equal(x2, h)
