@@ -18,7 +18,10 @@
 //
 // Bound: the way of a step's lines to LDS where a CU has one workgroup (0.61 us a
 // step), then the conversion and scaling of the sums, one for every 2 matrix
-// instructions of half rate (0.33 us for each workgroup more).
+// instructions of half rate (0.33 us for each workgroup more).  A buffer more, with
+// scales asked for two steps ahead, changed nothing (512 x 5120 x 5120 38.8 us against
+// 38.1), nor did tiles of 32 x 128 where there are few (256 rows 27.2 against 27.4; 64
+// rows 21.9 against 27.7, which the kernel for few rows takes in 13.6).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -91,15 +94,16 @@ __global__ __launch_bounds__(64 * WV, 2) void q8_blocks_kernel(Q8Args a, int til
     // codes.  Rows past the end, and steps past it, get an offset out of range and arrive as zeros.
     const int ar = lane >> 3, wr = lane >> 1;
     auto fetch = [&](uint8_t *to, int s) TERN_INLINE {
+        const int xs = s < groups ? s * 128 : OUT_OF_RANGE, ws = s < groups ? s * 32 : OUT_OF_RANGE;
 #pragma unroll
         for (int i = 0; i < T::AI; ++i) {
             const int at = wave * T::AI + i, row = at * 8 + ar, off = row * K + (((lane & 7) ^ xor128(row)) << 4);
-            load16_to_lds(rx, to + at * 1024, s < groups ? off + s * 128 : OUT_OF_RANGE);
+            load16_to_lds(rx, to + at * 1024, off + xs);
         }
 #pragma unroll
         for (int i = 0; i < T::WI; ++i) {
             const int at = wave * T::WI + i, row = at * 32 + wr, off = row * wrow + (((lane & 1) ^ xor32(row)) << 4);
-            load16_to_lds(rw, to + T::A_LDS + at * 1024, s < groups ? off + s * 32 : OUT_OF_RANGE);
+            load16_to_lds(rw, to + T::A_LDS + at * 1024, off + ws);
         }
     };
     // Scales go through registers, one step ahead of the tiles; past the end they are read again and

@@ -256,3 +256,22 @@ def test_large_products_in_two_graphs_and_on_two_streams():
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(y, w) for y, w in zip(out, want))
+
+
+# which of the kernels for more than 4 rows takes a size: few rows, 64 x 128 and 128 x 384 tiles, the
+# first two on either side of what the first can take (K >= 512)
+@pytest.mark.parametrize("M,N,K", [(5, 700, 384), (32, 1000, 384), (33, 640, 512), (65, 3000, 512), (97, 5120, 640),
+                                   (600, 1000, 384), (900, 2000, 640), (520, 5121, 1152)])
+@pytest.mark.parametrize("group", [0, 128])
+def test_rows_do_not_touch_each_other(M, N, K, group):
+    """Every row alone gives what it gives in the batch, to the last bits' order of sums; rows behind
+    the last stay as they were, and twice the same call is the same to the bit."""
+    print(f"matmul_q8 M={M} N={N} K={K} group={group}", flush=True)
+    q, xs, packed, ws = problem(M, N, K, group, M)
+    d = [dev(a) for a in (q, xs, packed, ws)]
+    y = run(q, xs, packed, ws, "f32")
+    assert torch.equal(y, tern.matmul_q8(*d, out_dtype=torch.float32))
+    rows = [0, M // 2, M - 1]
+    want, bound = R.product(q[rows], xs[rows], packed, ws, torch.float32)
+    R.assert_close(y[rows], want, bound, "rows of the batch")
+    R.assert_close(tern.matmul_q8(d[0][rows], d[1][rows], *d[2:], out_dtype=torch.float32), want, bound, "rows alone")
