@@ -16,9 +16,10 @@
 // Squares are summed in 64 bits: no row of any of the types leaves the range.  f is
 // applied as a power of two and the rest, so that it need not fit an fp32.
 //
-// Work layout.  A row stays in the registers of its threads, NV times 8 consecutive
-// values each, so that everything is read once and written once; a workgroup takes
-// rows in turn, keeps its weights, and asks for the next row while it works on one.
+// Work layout.  A row of up to 32768 values stays in the registers of its threads, NV
+// times 8 consecutive values each, so that everything is read once and written once;
+// a workgroup takes rows in turn, keeps its weights, and asks for the next row while
+// it works on one.
 // Rows of up to 1024 values are a wave's or a part of one and need no barrier,
 // longer ones one each.
 //
@@ -191,10 +192,8 @@ __device__ __forceinline__ float scale_of(uint32_t bits, double f) {
 template <int XT, int RT, int TPR, int NV, int MOST>
 __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
     constexpr int ROWS = TPR > 0 ? MOST / TPR : 1;
-    // Weights stay in registers, and the next row is asked for while this one is worked on, where there
-    // are registers for them.
-    constexpr bool HELD = NV <= 4, AHEAD = NV <= 3;
-    constexpr int TOGETHER = NV < 4 ? NV : 4;   // eights that are asked for at once
+    // The next row is asked for while this one is worked on, where there are registers for it.
+    constexpr bool AHEAD = NV <= 3;
     typedef typename Elem<XT>::type X;
     typedef typename Elem<(RT < 0 ? 0 : RT)>::type R;
     __shared__ double sums[2][16];
@@ -209,22 +208,12 @@ __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
         X x[8];
         R r[8];
     };
-    auto ask = [&](Eights (&e)[TOGETHER], int64_t row, int v0) __attribute__((always_inline)) {
+    auto ask = [&](Eights (&e)[NV], int64_t row) __attribute__((always_inline)) {
 #pragma unroll
-        for (int v = 0; v < TOGETHER; ++v)
-            __builtin_memcpy(e[v].x, static_cast<const X *>(a.X) + row * K + first(v0 + v), sizeof(e[v].x));
+        for (int v = 0; v < NV; ++v) __builtin_memcpy(e[v].x, static_cast<const X *>(a.X) + row * K + first(v), sizeof(e[v].x));
         if constexpr (RT >= 0) {
 #pragma unroll
-            for (int v = 0; v < TOGETHER; ++v)
-                __builtin_memcpy(e[v].r, static_cast<const R *>(a.R) + row * K + first(v0 + v), sizeof(e[v].r));
-        }
-    };
-    auto weights = [&](int v, float (&w)[8]) __attribute__((always_inline)) {
-        if (a.W != nullptr) {
-            load8_any(a.W, a.w_dtype, first(v), w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 1.f;
+            for (int v = 0; v < NV; ++v) __builtin_memcpy(e[v].r, static_cast<const R *>(a.R) + row * K + first(v), sizeof(e[v].r));
         }
     };
     // every thread of a workgroup takes part in each turn: rows past the last one are read as row M - 1
@@ -232,12 +221,17 @@ __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
     auto mine = [&](int64_t row0) __attribute__((always_inline)) { return min(row0 + my_row, a.M - 1); };
     const double per = 1.0 / K;
     int64_t row0 = (int64_t)blockIdx.x * ROWS;
-    Eights e[TOGETHER];
-    ask(e, mine(row0), 0);
-    float held[HELD ? NV : 1][8];
-    if constexpr (HELD) {
+    Eights e[NV];
+    ask(e, mine(row0));
+    float w[NV][8];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) weights(v, held[v]);
+    for (int v = 0; v < NV; ++v) {
+        if (a.W != nullptr) {
+            load8_any(a.W, a.w_dtype, first(v), w[v]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[v][i] = 1.f;
+        }
     }
     int slot = 0;
     for (;;) {
@@ -247,18 +241,14 @@ __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
         float h[NV][8];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (v > 0 && v % TOGETHER == 0) {
-                __builtin_amdgcn_sched_barrier(0);   // not before: there are no registers
-                ask(e, row, v);
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[v][i] = (float)e[v % TOGETHER].x[i];
-                if constexpr (RT >= 0) h[v][i] = (float)(R)(h[v][i] + (float)e[v % TOGETHER].r[i]);
+                h[v][i] = (float)e[v].x[i];
+                if constexpr (RT >= 0) h[v][i] = (float)(R)(h[v][i] + (float)e[v].r[i]);
             }
         }
         if constexpr (AHEAD) {
-            if (row0 < a.M) ask(e, mine(row0), 0);
+            if (row0 < a.M) ask(e, mine(row0));
         }
         double sum = 0;
 #pragma unroll
@@ -283,12 +273,9 @@ __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
         if (coded) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                float again[8];
-                if constexpr (!HELD) weights(v, again);
-                const float(&w)[8] = HELD ? held[HELD ? v : 0] : again;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    top[v] = max(top[v], __builtin_bit_cast(uint32_t, h[v][i] * w[i]) & 0x7FFFFFFFu);
+                    top[v] = max(top[v], __builtin_bit_cast(uint32_t, h[v][i] * w[v][i]) & 0x7FFFFFFFu);
             }
             if (grouped) {   // 128 values are 16 lanes' 8
 #pragma unroll
@@ -324,24 +311,146 @@ __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
             if (!there || (v * threads + t) * 8 >= K) continue;
             // all of the row has been read by now: H may be R
             if constexpr (RT >= 0) store8_of(static_cast<R *>(a.H) + at + k, h[v]);
-            float again[8];
-            if constexpr (!HELD) weights(v, again);
-            const float(&w)[8] = HELD ? held[HELD ? v : 0] : again;
             if (a.Y != nullptr) {
                 float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = h[v][i] * f.f1 * f.f2 * w[i];
+                for (int i = 0; i < 8; ++i) y[i] = h[v][i] * f.f1 * f.f2 * w[v][i];
                 store8_any(a.Y, a.y_dtype, at + k, y);
             }
             if (coded) {
                 const uint32_t bits = grouped ? top[v] : top[0];
-                const uint64_t q = has_codes(bits) ? codes_of(h[v], w, __builtin_bit_cast(float, bits)) : 0;
+                const uint64_t q = has_codes(bits) ? codes_of(h[v], w[v], __builtin_bit_cast(float, bits)) : 0;
                 __builtin_memcpy(a.Q + at + k, &q, 8);
                 if (t % 16 == 0 && (grouped || v * threads + t == 0)) a.S[grouped ? (at + k) / 128 : row] = scale_of(bits, f.f);
             }
         }
         if (row0 >= a.M) break;
-        if constexpr (!AHEAD) ask(e, mine(row0), 0);
+        if constexpr (!AHEAD) ask(e, mine(row0));
+    }
+}
+
+// Rows too long for registers: a workgroup of 1024 reads one twice, the second time from the L2 (64 rows of
+// 65536 to 8 bits 46 us; with what did not fit in registers in scratch memory 72).  8 values
+// a thread in turn, 4 turns' asked for at once; the last ones one by one, as the stream may be written in
+// place and no value may be read after that as if it were x or r.
+template <int XT, int RT>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
+    constexpr int NT = 1024, TOGETHER = 4;
+    typedef typename Elem<XT>::type X;
+    typedef typename Elem<(RT < 0 ? XT : RT)>::type R;   // of the stream
+    __shared__ double sums[2][16];
+    __shared__ uint32_t tops[2][16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = (int)a.K;
+    const bool grouped = a.grouped != 0, coded = a.Q != nullptr;
+    auto load = [&](const auto *from, int k, auto (&e)[8]) __attribute__((always_inline)) {
+        if (k + 8 <= K) {
+            __builtin_memcpy(e, from + k, sizeof(e));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = k + i < K ? from[k + i] : 0;
+        }
+    };
+    auto weights = [&](int k, float (&w)[8]) __attribute__((always_inline)) {
+        if (a.W != nullptr && k + 8 <= K) {
+            load8_any(a.W, a.w_dtype, k, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = a.W != nullptr && k + i < K ? load_any(a.W, a.w_dtype, k + i) : 1.f;
+        }
+    };
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+        const int64_t at = row * K;
+        const X *x = static_cast<const X *>(a.X) + at;
+        double sum = 0;
+        uint32_t top = 0;
+        for (int k0 = tid * 8; k0 < K; k0 += TOGETHER * NT * 8) {
+            X ex[TOGETHER][8];
+            R er[TOGETHER][8];
+#pragma unroll
+            for (int v = 0; v < TOGETHER; ++v) {
+                load(x, k0 + v * NT * 8, ex[v]);
+                if constexpr (RT >= 0) load(static_cast<const R *>(a.R) + at, k0 + v * NT * 8, er[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < TOGETHER; ++v) {
+                const int k = k0 + v * NT * 8;
+                float h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] = (float)ex[v][i];
+                    if constexpr (RT >= 0) h[i] = (float)(R)(h[i] + (float)er[v][i]);
+                    sum = __builtin_fma((double)h[i], (double)h[i], sum);   // zeros past the end
+                }
+                if constexpr (RT >= 0) {
+                    R *stream = static_cast<R *>(a.H) + at;
+                    if (k + 8 <= K) {
+                        store8_of(stream + k, h);
+                    } else {
+                        for (int i = 0; i < 8; ++i)
+                            if (k + i < K) stream[k + i] = (R)h[i];
+                    }
+                }
+                if (coded && !grouped) {
+                    float w[8];
+                    weights(k, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, h[i] * w[i]) & 0x7FFFFFFFu);
+                }
+            }
+        }
+        sum = row_sum(sum), top = row_max(top);
+        sum = (lane_of(sum, 0) + lane_of(sum, 16)) + (lane_of(sum, 32) + lane_of(sum, 48));
+        top = max(max(lane_of(top, 0), lane_of(top, 16)), max(lane_of(top, 32), lane_of(top, 48)));
+        if (lane == 0) sums[slot][wave] = sum, tops[slot][wave] = top;
+        wait_and_meet<63>();   // as above
+        sum = row_sum(sums[slot][lane & 15]), top = row_max(tops[slot][lane & 15]);
+        slot ^= 1;
+        const Factor f = factor_of(sum, 1.0 / K, (double)a.eps, a.normalize != 0);
+        if (coded && !grouped && tid == 0) a.S[row] = scale_of(top, f.f);
+        const R *stream = static_cast<const R *>(RT >= 0 ? a.H : a.X) + at;
+        for (int k0 = tid * 8; k0 < K; k0 += TOGETHER * NT * 8) {
+            R e[TOGETHER][8];
+#pragma unroll
+            for (int v = 0; v < TOGETHER; ++v) load(stream, k0 + v * NT * 8, e[v]);
+#pragma unroll
+            for (int v = 0; v < TOGETHER; ++v) {
+                const int k = k0 + v * NT * 8;
+                if (k >= K) continue;
+                float h[8], w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = (float)e[v][i];
+                weights(k, w);
+                if (a.Y != nullptr) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = h[i] * f.f1 * f.f2 * w[i];
+                    if (k + 8 <= K) {
+                        store8_any(a.Y, a.y_dtype, at + k, y);
+                    } else {
+                        for (int i = 0; i < K - k; ++i) store_any(a.Y, a.y_dtype, at + k + i, y[i]);
+                    }
+                }
+                if (coded) {
+                    uint32_t bits = top;
+                    if (grouped) {   // 128 values are 16 lanes' 8, all of them here
+                        bits = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) bits = max(bits, __builtin_bit_cast(uint32_t, h[i] * w[i]) & 0x7FFFFFFFu);
+                        bits = row_max(bits);
+                        if (tid % 16 == 0) a.S[(at + k) / 128] = scale_of(bits, f.f);
+                    }
+                    const uint64_t q = has_codes(bits) ? codes_of(h, w, __builtin_bit_cast(float, bits)) : 0;
+                    if (k + 8 <= K) {
+                        __builtin_memcpy(a.Q + at + k, &q, 8);
+                    } else {
+                        for (int i = 0; i < K - k; ++i) a.Q[at + k + i] = (int8_t)(q >> (8 * i));
+                    }
+                }
+            }
+        }
     }
 }
 
@@ -407,7 +516,8 @@ hipError_t launch_row(const NormArgs &a) {
     if (a.K <= 8192) return launch_t<XT, RT, 0, 2, 512>(a);
     if (a.K <= 12288) return launch_t<XT, RT, 0, 3, 512>(a);
     if (a.K <= 32768) return launch_t<XT, RT, 0, 4, 1024>(a);
-    return launch_t<XT, RT, 0, 8, 1024>(a);
+    hipLaunchKernelGGL((norm_long_kernel<XT, RT>), dim3((unsigned)std::min<int64_t>(a.M, 512)), dim3(1024), 0, a.stream, a);
+    return hipGetLastError();
 }
 
 template <int YT>

@@ -9,7 +9,7 @@
 
 namespace tern {
 
-constexpr int64_t kNormMaxK = 65536;   // a row stays in the registers of one workgroup
+constexpr int64_t kNormMaxK = 65536;   // a row is one workgroup's
 
 struct NormArgs {
     const void *X;      // [M,K]
