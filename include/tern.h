@@ -347,8 +347,8 @@ tern_status tern_q8_dequant(const int8_t *codes, const float *scales, int32_t q_
  *   Y[m,n] = sum over blocks g of 128 of x_scale[m,g] S[n,g] * sum over k in g of code[m,k] t[n,k]
  * The inner sums are exact integers; the rest is fp32, rounded once.  Any codes
  * from -128 to 127 and any scales.  packed_W, scales and group as tern_matmul;
- * x_codes 16-byte, x_scales 4-byte aligned; K <= 2^23, M and N <= 2^28.  A NaN or
- * infinite scale reaches its own row or column of Y only.
+ * x_codes 16-byte, x_scales 4-byte aligned; K <= 2^23, M and N <= 2^28, M N <=
+ * 2^36.  A NaN or infinite scale reaches its own row or column of Y only.
  *   workspace: tern_matmul_q8_workspace bytes (TERN_ERR_SHAPE if fewer; for a large
  *       product some 1.5 K for each row of X, else none, never for 32 rows or
  *       fewer), 16-byte aligned, for this call alone until the stream has passed it.

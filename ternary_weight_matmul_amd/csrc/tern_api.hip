@@ -18,8 +18,8 @@ constexpr int64_t kMaxK = int64_t(1) << 30;
 // of K / 2 bytes).
 constexpr int64_t kMxMaxK = int64_t(1) << 24;
 // Products with 8-bit activations: the same, 128 rows of K bytes; a grid has fewer than 2^32 threads,
-// and that of few rows up to 8 for each row of W.
-constexpr int64_t kQ8MaxK = int64_t(1) << 23, kQ8MaxDim = int64_t(1) << 28;
+// up to 8 for each row of W with few rows of X, and one for 32 outputs in tiles of 64 x 128.
+constexpr int64_t kQ8MaxK = int64_t(1) << 23, kQ8MaxDim = int64_t(1) << 28, kQ8MaxOut = int64_t(1) << 36;
 constexpr int64_t kMaxProduct = int64_t(1) << 62;
 constexpr size_t kGemvLdsLimit = 152 * 1024;
 
@@ -221,7 +221,7 @@ tern_status check_q8_pointers(const int8_t *codes, const float *scales) {
 }
 
 bool q8_product_ok(int64_t M, int64_t N, int64_t K) {
-    return M >= 0 && N >= 0 && K >= 0 && M <= kQ8MaxDim && N <= kQ8MaxDim && K <= kQ8MaxK && product_ok(M, N);
+    return M >= 0 && N >= 0 && K >= 0 && M <= kQ8MaxDim && N <= kQ8MaxDim && K <= kQ8MaxK && M * N <= kQ8MaxOut;
 }
 
 // Which kernel takes a product with 8-bit activations: the decode kernel of up to 4 rows; the one for

@@ -60,7 +60,8 @@ def mm(C=P, XS=P, qg=0, W=P, S=P, Y=P, yd=BF16, M=2, N=16, K=256, G=128, ws=0, w
 
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-128), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=1 << 31), SHAPE),
-    (dict(K=(1 << 23) + 128), SHAPE), (dict(M=(1 << 28) + 1), SHAPE), (dict(N=(1 << 28) + 1), SHAPE), (dict(K=200), GROUP), (dict(G=0), GROUP), (dict(G=-128), GROUP), (dict(G=64), UNSUP),
+    (dict(K=(1 << 23) + 128), SHAPE), (dict(M=(1 << 28) + 1), SHAPE), (dict(N=(1 << 28) + 1), SHAPE),
+    (dict(M=1 << 20, N=(1 << 16) + 1), SHAPE), (dict(K=200), GROUP), (dict(G=0), GROUP), (dict(G=-128), GROUP), (dict(G=64), UNSUP),
     (dict(qg=64), UNSUP), (dict(qg=-128), UNSUP), (dict(yd=3), DTYPE), (dict(C=0), NULL), (dict(XS=0), NULL),
     (dict(W=0), NULL), (dict(S=0), NULL), (dict(Y=0), NULL), (dict(K=0, Y=0), NULL), (dict(C=P + 8), ALIGN),
     (dict(XS=P + 2), ALIGN), (dict(W=P + 8), ALIGN), (dict(S=P + 1), ALIGN), (dict(Y=P + 1), ALIGN),
@@ -79,7 +80,7 @@ def test_matmul_q8_workspace():
     assert mm(**big, ws=P, wb=need - 1) == SHAPE
     assert mm(**big, ws=P + 8, wb=need) == ALIGN
     for bad in ((-1, 4, 128), (300, -4, 128), (300, 64, -128), (300, 64, 100), (0, 64, 128), (300, 0, 128), (300, 64, 0),
-                ((1 << 28) + 1, 64, 128), (300, (1 << 28) + 1, 128)):
+                ((1 << 28) + 1, 64, 128), (300, (1 << 28) + 1, 128), (1 << 20, (1 << 16) + 1, 128)):
         assert L.tern_matmul_q8_workspace(*bad) == 0
 
 
