@@ -9,8 +9,9 @@
 // activations and scales stay on chip (§4.2, §4.3).
 //
 // 8-bit activations are split into two e4m3 terms of scale 1 (tern_fp4.h), so that
-// a block's sum is the exact integer; the block's activation scales (or their row's,
-// read for every block) join the weights' there.
+// a block's sum is the exact integer.  It meets the weights' scale first, which keeps it
+// within 2^-24 and 2^30, and then the activations' (of the block, or at the end that of
+// the row): any scale of theirs leaves fp32 only where the result does.
 //
 // Operands (tern_fp4.h): the weights as e2m1 +-2 / 0 (B; 10 VALU operations
 // per 32 weights, about a third of a lane-op per weight against 0.9 for
@@ -97,15 +98,15 @@ constexpr int step_lds() {
     return 8 * M * (F_IMG + 4);
 }
 
-// XQ: X holds int8 codes, Rf their scales: that of row m and block g at m xm + g xg.
-template <int M, bool S8, bool XQ, int Q, int SPW>
+// XQ: X holds int8 codes, Rf their scales, 1: [M], 2: [M,K/128].
+template <int M, bool S8, int XQ, int Q, int SPW>
 __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *__restrict__ Xv,
                                                                   const uint8_t *__restrict__ P,
                                                                   const uint16_t *__restrict__ S,
                                                                   const int8_t *__restrict__ Qs,
                                                                   const float *__restrict__ Rf, void *__restrict__ Y,
-                                                                  int y_dtype, int N, int K, int xm, int xg) {
-    static_assert(!(S8 && XQ), "one kind of scales beside the weights' fp16 ones");
+                                                                  int y_dtype, int N, int K) {
+    static_assert(!(S8 && XQ != 0), "one kind of scales beside the weights' fp16 ones");
     constexpr int IMGS = 8 * M;
     constexpr int SL = step_lds<M>();
     constexpr bool ONE = M <= 2;   // hi and lo terms in one MFMA
@@ -137,16 +138,21 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
     //         scale load of the wave (rows past N read zeros; bytes past K
     //         meet zero activations, and their scales are dropped) ----
     uint4 xq[SPW][M];      // 8 bf16, or 8 codes in the first two words
-    float xs[SPW][M];
+    float xs[SPW][M];      // XQ 2: the blocks' scales
+    float row_scale[M];    // XQ 1
+    if constexpr (XQ == 1) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) row_scale[m] = Rf[m];
+    }
 #pragma unroll
     for (int st = 0; st < SPW; ++st) {
         const int k0 = min((wave * SPW + st) * F_STEP + 8 * lane, K - 8);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            if constexpr (XQ) {
+            if constexpr (XQ != 0) {
                 const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(Xv) + (int64_t)m * K + k0);
                 xq[st][m] = make_uint4(v.x, v.y, 0, 0);
-                xs[st][m] = Rf[m * xm + min(4 * (wave * SPW + st) + c, groups - 1) * xg];
+                if constexpr (XQ == 2) xs[st][m] = Rf[m * groups + min(4 * (wave * SPW + st) + c, groups - 1)];
             } else {
                 xq[st][m] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(Xv) + (int64_t)m * K + k0);
             }
@@ -229,7 +235,7 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
             xv.y &= keep;
             uint32_t eh, el;   // the 32-run's hi and lo scale exponents
             uint32_t he, ho, le, lo;
-            if constexpr (XQ) {
+            if constexpr (XQ != 0) {
                 split8_codes(xv.x, xv.y, he, ho, le, lo);
             } else {
                 xv.z &= keep;
@@ -245,7 +251,7 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
             *reinterpret_cast<uint32_t *>(wimg + il * F_IMG + loff + 8) = lo;
             // one lane of the quad writes the run's scale bytes (the others a
             // spare byte: no branch around the stores)
-            if constexpr (!XQ) {
+            if constexpr (XQ == 0) {
                 *(so == 0 ? wimg + IMGS * F_IMG + ih * 4 + su : spare_byte) = (char)eh;
                 *(so == 0 ? wimg + IMGS * F_IMG + il * 4 + su : spare_byte) = (char)el;
             }
@@ -262,7 +268,7 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
             const uint4 d0 = *reinterpret_cast<const uint4 *>(wimg + img * F_IMG + p * 32);
             const uint4 d1 = *reinterpret_cast<const uint4 *>(wimg + img * F_IMG + p * 32 + 16);
             a[h] = (int8v_t){(int)d0.x, (int)d0.y, (int)d0.z, (int)d0.w, (int)d1.x, (int)d1.y, (int)d1.z, (int)d1.w};
-            sa[h] = XQ ? 127u : (unsigned char)wimg[IMGS * F_IMG + img * 4 + p];
+            sa[h] = XQ != 0 ? 127u : (unsigned char)wimg[IMGS * F_IMG + img * 4 + p];
         }
         const bool blk_ok = 4 * s + c < groups;
 #pragma unroll
@@ -273,10 +279,13 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
             if constexpr (!ONE) d = mfma_f8f4(a[1], bw, d, sa[1]);
             float sc = S8 ? (float)(int32_t)sbits[st][q] : f16_bits_to_float((uint16_t)sbits[st][q]);
             sc = blk_ok ? sc : 0.f;
+            if constexpr (XQ != 0) sc *= 0.5f;   // the weights are +-2
 #pragma unroll
-            for (int m = 0; m < M; ++m)
+            for (int m = 0; m < M; ++m) {
+                const float e = ONE ? d[m] + d[2 + m] : d[m];
                 // past K the scales are another block's, and need not be finite
-                acc[q][m] = fmaf(XQ ? (blk_ok ? sc * xs[st][m] : 0.f) : sc, ONE ? d[m] + d[2 + m] : d[m], acc[q][m]);
+                acc[q][m] = XQ == 2 ? fmaf(e * sc, blk_ok ? xs[st][m] : 0.f, acc[q][m]) : fmaf(sc, e, acc[q][m]);
+            }
         }
     }
 #pragma unroll
@@ -311,7 +320,13 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
     auto finish = [&](int m, int rr, float y) {
         const int n = n0 + rr;
         if (n >= N) return;
-        y *= 0.5f;   // the weights were +-2
+        if constexpr (XQ == 0) y *= 0.5f;   // the weights were +-2
+        if constexpr (XQ == 1) {
+            float f = row_scale[0];
+#pragma unroll
+            for (int i = 1; i < M; ++i) f = m == i ? row_scale[i] : f;
+            y *= f;
+        }
         if constexpr (S8) y *= Rf[n];
         if (y_dtype == 2) store_out<2>(Y, (int64_t)m * N + n, y);
         else if (y_dtype == 1) store_out<1>(Y, (int64_t)m * N + n, y);
@@ -400,7 +415,7 @@ F4Shape f4_shape(int64_t M, int64_t N, int64_t K) {
     return g;
 }
 
-template <int M, bool S8, bool XQ, int Q, int SPW>
+template <int M, bool S8, int XQ, int Q, int SPW>
 hipError_t launch_f4t(const GemmArgs &a, const F4Shape &g) {
     auto kern = gemv_fp4_kernel<M, S8, XQ, Q, SPW>;
     if (g.lds > 64 * 1024) {
@@ -419,12 +434,11 @@ hipError_t launch_f4t(const GemmArgs &a, const F4Shape &g) {
         }
     }
     hipLaunchKernelGGL(kern, dim3((unsigned)g.grid), dim3(64 * g.nw), g.lds, a.stream,
-                       a.X, a.W, a.S, a.Q, a.R, a.Y, a.y_dtype, (int)a.N, (int)a.K,
-                       a.x_grouped ? (int)(a.K >> 7) : 1, a.x_grouped ? 1 : 0);
+                       a.X, a.W, a.S, a.Q, a.R, a.Y, a.y_dtype, (int)a.N, (int)a.K);
     return hipGetLastError();
 }
 
-template <int M, bool S8, bool XQ>
+template <int M, bool S8, int XQ>
 hipError_t launch_f4s(const GemmArgs &a, const F4Shape &g) {
 #define TERN_F4_CASE(SP, QQ) \
     if (g.spw == SP && g.q == QQ) return launch_f4t<M, S8, XQ, QQ, SP>(a, g);
@@ -435,8 +449,8 @@ hipError_t launch_f4s(const GemmArgs &a, const F4Shape &g) {
 
 template <int M>
 hipError_t launch_f4m(const GemmArgs &a, const F4Shape &g) {
-    if (a.x_dtype == 3) return launch_f4s<M, false, true>(a, g);
-    return a.Q != nullptr ? launch_f4s<M, true, false>(a, g) : launch_f4s<M, false, false>(a, g);
+    if (a.x_dtype == 3) return a.x_grouped ? launch_f4s<M, false, 2>(a, g) : launch_f4s<M, false, 1>(a, g);
+    return a.Q != nullptr ? launch_f4s<M, true, 0>(a, g) : launch_f4s<M, false, 0>(a, g);
 }
 
 }  // namespace

@@ -161,8 +161,9 @@ __global__ __launch_bounds__(64 * WV, 2) void q8_blocks_kernel(Q8Args a, int til
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float e = GX ? (float)d[m & 1][n][v] * xs[m & 1] : (float)d[m & 1][n][v];
-                    acc[n][m][v] = fmaf(e, sc[n][v], acc[n][m][v]);
+                    // the weights' scale first: the other may be anything
+                    const float e = GX ? (float)d[m & 1][n][v] * sc[n][v] : (float)d[m & 1][n][v];
+                    acc[n][m][v] = fmaf(e, GX ? xs[m & 1] : sc[n][v], acc[n][m][v]);
                 }
         };
         read(0);

@@ -291,8 +291,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_ker
         auto scale = [&](int t) TERN_INLINE {   // tile t = m NB + n
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
-                const float e = GX ? d[t & 1][v] * xs[GX ? t / NB : 0][v] : d[t & 1][v];
-                acc[t / NB][t % NB][v] = fmaf(e, sc[t % NB], acc[t / NB][t % NB][v]);
+                // the weights' scale first: the other may be anything
+                const float e = GX ? d[t & 1][v] * sc[t % NB] : d[t & 1][v];
+                acc[t / NB][t % NB][v] = fmaf(e, GX ? xs[GX ? t / NB : 0][v] : sc[t % NB], acc[t / NB][t % NB][v]);
             }
         };
 #pragma unroll

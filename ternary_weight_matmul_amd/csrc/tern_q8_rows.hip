@@ -138,10 +138,11 @@ __global__ __launch_bounds__(64 * RW * KW) void q8_rows_kernel(Q8Args a) {
                 const int4v_t d = mfma_i8(x1, w1, mfma_i8(x0, w0, (int4v_t){0, 0, 0, 0}));
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    float e = (float)d[v];
+                    float e = (float)d[v], s = scale[g];   // 0 past the end
+                    // the weights' scale first: the other may be anything
                     if constexpr (GX)
-                        e *= *reinterpret_cast<const float *>(x + T::S_AT + ((16 * m + 4 * p + v) * 4 + g) * 4);
-                    acc[m][v] = fmaf(e, scale[g], acc[m][v]);   // scales past the end are 0
+                        e *= s, s = *reinterpret_cast<const float *>(x + T::S_AT + ((16 * m + 4 * p + v) * 4 + g) * 4);
+                    acc[m][v] = fmaf(e, s, acc[m][v]);
                 }
             }
         }
