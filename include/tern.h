@@ -305,8 +305,9 @@ tern_status tern_moe(const void *X, tern_dtype x_dtype, const void *logits, tern
  *   TERN_ERR_GROUP otherwise; any other q_group is TERN_ERR_UNSUPPORTED);
  *   the value is code * scale.
  * What is made here has a scale a / 127 for a row or block whose largest
- * magnitude is a, and codes 127 v / a rounded to nearest, ties to even: in
- * [-127, 127], and always the same for the same values.  A block of zeros has
+ * magnitude is a, and codes 127 v / a rounded to nearest, ties to even, and cut
+ * off at 127 (an a below 2^-126 is an fp32 of few bits, and may be less than |v|):
+ * in [-127, 127], and always the same for the same values.  A block of zeros has
  * the scale 0.  One with an infinity or a NaN has the scale NaN and codes 0.
  */
 

@@ -152,7 +152,9 @@ __device__ __forceinline__ uint64_t codes_of(const float (&h)[8], const float (&
             float hi = h[0], wi = w[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) hi = i == j ? h[j] : hi, wi = i == j ? w[j] : wi;
-            const uint32_t c = (uint32_t)(int)__builtin_rint(127.0 * ((double)hi * (double)wi) / (double)a);
+            // an a below the normal range may be a third less than the value that it stands for
+            const double q = __builtin_rint(127.0 * ((double)hi * (double)wi) / (double)a);
+            const uint32_t c = (uint32_t)(int)fmin(fmax(q, -127.0), 127.0);
 #pragma unroll
             for (int j = 0; j < 8; ++j) n[j] = i == j ? c : n[j];
         }

@@ -1,0 +1,77 @@
+"""Codes of 8-bit activations whose magnitudes are so small that the largest of them loses bits as
+an fp32.  The reference decides values next to a border between two codes in exact arithmetic."""
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import q8_util as R  # noqa: E402
+
+tern = pytest.importorskip("ternary_weight_matmul_amd")
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def exact_codes(h, w, group):
+    """Codes of h w (h [M,K] and w [K] hold fp32 values): 127 h w / a to nearest even, at most 127."""
+    p = h * w                                           # 48 bits: exact
+    b = R.blocks(p, group)
+    a = np.abs(b).max(-1, keepdims=True).astype(np.float32).astype(np.float64)
+    v = 127.0 * b / np.where(a > 0, a, 1.0)
+    q = np.rint(v)
+    near = np.abs(np.abs(v - np.floor(v)) - 0.5) < 2.0 ** -30
+    for i in zip(*np.nonzero(near)):
+        q[i] = round(127 * Fraction(b[i]) / Fraction(a[i[0], i[1], 0]))   # to nearest, ties to even
+    q = np.clip(np.where(a > 0, q, 0.0), -127, 127)
+    assert np.abs(q).max() <= 127
+    return q.reshape(h.shape).astype(np.int8)
+
+
+def check(x, w, group, eps=0.0):
+    """x [M,K], w [K] fp32 tensors."""
+    codes, scales = tern.rms_norm_q8(x.to(DEV), w.to(DEV), eps=eps, group=group)
+    want = exact_codes(R.f64(x), R.f64(w), group)
+    got = codes.cpu().numpy()
+    bad = np.nonzero(got != want)
+    assert bad[0].size == 0, (got[bad][:8], want[bad][:8], [i[:8] for i in bad])
+    return scales
+
+
+@pytest.mark.parametrize("K", [4, 17, 128, 512, 1280, 9000, 20000, 40000])
+@pytest.mark.parametrize("group", [0, 128])
+def test_codes_of_magnitudes_below_the_normal_range(K, group):
+    """The largest magnitude as an fp32 is up to a third below the value: its code is 127, not 178."""
+    if K % 128 and group:
+        pytest.skip("a group divides K")
+    print(f"small magnitudes K={K} group={group}", flush=True)
+    rng = np.random.default_rng(K)
+    for top in (1.4, -1.4, 1.49, 2.4, 3.49, -7.4, 12.5, 100.3):
+        x = torch.from_numpy(rng.uniform(-1, 1, (3, K))).float() * 2.0 ** -100
+        w = torch.full((K,), abs(top) * 2.0 ** -49)
+        x[:, ::3] = 2.0 ** -100 if top > 0 else -2.0 ** -100
+        check(x, w, group)
+
+
+def test_codes_of_quantize_below_the_normal_range():
+    x = torch.from_numpy(np.random.default_rng(1).integers(-9, 10, (4, 256)) * 2.0 ** -149).float()
+    for group in (0, 128):
+        codes, _ = tern.q8_quantize(x.to(DEV), group=group)
+        assert np.array_equal(codes.cpu().numpy(), exact_codes(R.f64(x), np.ones(256), group))
+
+
+@pytest.mark.parametrize("M,K", [(50, 128), (9, 1000), (7, 5120), (3, 20000), (2, 40000)])
+def test_codes_of_ordinary_values(M, K):
+    rng = np.random.default_rng(M)
+    x = torch.from_numpy(rng.standard_normal((M, K))).float()
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(K)).float()
+    for group in ((0,) if K % 128 else (0, 128)):
+        check(x, w, group, 1e-6)

@@ -1,0 +1,71 @@
+"""Routing where scores are not numbers or experts are missing, and the expert layer with more
+routes than experts."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import q8_util as R  # noqa: E402
+from test_gpu_route import DT, Layer, check  # noqa: E402
+
+tern = pytest.importorskip("ternary_weight_matmul_amd")
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("groups,keep,best", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_logits_that_are_not_finite(score, biased, groups, keep, best, renorm):
+    """A softmax over +inf or NaN has NaN weights, whichever experts are taken."""
+    E = 32
+    rng = np.random.default_rng(11)
+    lg = torch.from_numpy(rng.standard_normal((6, E))).float()
+    lg[0, 3] = INF
+    lg[1, 29], lg[1, 30] = INF, INF
+    lg[2, 17] = NAN
+    lg[3, 8:] = -INF
+    lg[3, 5] = INF
+    lg[4, :31], lg[4, 31] = -INF, NAN
+    bias = torch.from_numpy(rng.standard_normal(E) * 0.1).float() if biased else None
+    check(lg, 8, score, bias, groups, keep, best, renorm, 2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("scale", [1.0, INF, -INF, NAN])
+def test_places_without_an_expert_have_no_weight(score, biased, renorm, scale):
+    """ids -1 come with weight 0, also beside NaN weights and with any factor."""
+    E = 16
+    lg = torch.full((4, E), -INF)
+    lg[0, 2] = NAN
+    lg[1, 4] = INF
+    lg[2, 5], lg[2, 9] = 0.25, -1.5
+    bias = torch.linspace(-0.1, 0.1, E) if biased else None
+    ids, w = check(lg, 6, score, bias, 1, 1, 1, renorm, scale)
+    assert (w[ids < 0] == 0).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 3, 8), (4, 3, 8), (5, 3, 8), (70, 3, 8), (1, 1, 32), (4, 1, 32), (5, 1, 32), (70, 1, 32),
+                                   (3, 5, 31), (20, 2, 17)])
+@pytest.mark.parametrize("xd,yd", [("bf16", "bf16"), ("f16", "f32")])
+def test_more_routes_than_experts(T, E, k, xd, yd):
+    """An expert that is taken many times has the sum of its weights."""
+    print(f"routed T={T} E={E} k={k} {xd}->{yd}", flush=True)
+    H, F = 384, 256
+    L = Layer(E, H, F, T + E)
+    rng = np.random.default_rng(T + k)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(DT[xd])
+    ids = torch.from_numpy(rng.integers(-1, E + 1, (T, k)).astype(np.int32))
+    w = torch.from_numpy(rng.standard_normal((T, k))).float()
+    want, bound = L.want(x, ids, w, yd)
+    R.assert_close(L.run(x, ids, w, yd), want, bound, "more routes than experts")
