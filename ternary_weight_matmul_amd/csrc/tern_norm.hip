@@ -10,8 +10,10 @@
 // follow from h and w alone, and are the same on every machine and in any order
 // of the sum.  a is held as an fp32, h w is taken exactly.  In fp32 127 h w / a is
 // off by less than 2^-15 (three roundings of a value up to 127): where that could
-// change the code, one value in 16000, it is formed anew in 64 bits, in which the
-// quotient of these numbers is rounded to the right side of any border.
+// change the code, one value in 16000, it is decided in 64 bits: h w is exact there,
+// and so is any border (n + 1/2) a, so that one fused multiply-add tells on which side
+// of it 127 h w lies.  (The quotient itself may round to the border: 127 h w has up to
+// 55 bits.)
 //
 // Squares are summed in 64 bits: no row of any of the types leaves the range.  f is
 // applied as a power of two and the rest, so that it need not fit an fp32.
@@ -152,9 +154,12 @@ __device__ __forceinline__ uint64_t codes_of(const float (&h)[8], const float (&
             float hi = h[0], wi = w[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) hi = i == j ? h[j] : hi, wi = i == j ? w[j] : wi;
+            const double p = (double)hi * (double)wi;
             // an a below the normal range may be a third less than the value that it stands for
-            const double q = __builtin_rint(127.0 * ((double)hi * (double)wi) / (double)a);
-            const uint32_t c = (uint32_t)(int)fmin(fmax(q, -127.0), 127.0);
+            const int below = (int)fmin(fmax(floor(127.0 * p / (double)a), -128.0), 127.0);
+            // (below + 1/2) a is exact, and its difference to 127 p has the right sign
+            const double past = __builtin_fma(127.0, p, -((double)below + 0.5) * (double)a);
+            const uint32_t c = (uint32_t)max(min(below + (past > 0.0 || (past == 0.0 && (below & 1))), 127), -127);
 #pragma unroll
             for (int j = 0; j < 8; ++j) n[j] = i == j ? c : n[j];
         }

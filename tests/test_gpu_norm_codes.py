@@ -1,5 +1,6 @@
-"""Codes of 8-bit activations whose magnitudes are so small that the largest of them loses bits as
-an fp32.  The reference decides values next to a border between two codes in exact arithmetic."""
+"""Codes of 8-bit activations where the 64-bit quotient is not enough: values that lie next to
+a border between two codes by less than it shows, and magnitudes so small that the largest of
+them loses bits as an fp32.  The reference decides such values in exact arithmetic."""
 from fractions import Fraction
 
 import numpy as np
@@ -44,6 +45,42 @@ def check(x, w, group, eps=0.0):
     bad = np.nonzero(got != want)
     assert bad[0].size == 0, (got[bad][:8], want[bad][:8], [i[:8] for i in bad])
     return scales
+
+
+def near_borders(count, seed):
+    """(h, w, A) whose 127 h w / a, a = A 2^24, lies next to a border by so little that its 64-bit
+    quotient is the border itself, and rounds to the wrong side."""
+    rng = np.random.default_rng(seed)
+    found = []
+    while len(found) < count:
+        n, d = int(rng.integers(70, 127)), int(rng.choice([-1, 1]))
+        h = int(rng.integers(1 << 22, 1 << 23)) * 2 + 1
+        m = (2 * n + 1) << 23
+        if h % 127 == 0 or np.gcd(127 * h, m) > 1:
+            continue
+        w = d * pow(127 * h, -1, m) % m                 # 127 h w = d + A m
+        A = (127 * h * w - d) // m
+        if w >= 1 << 24 or not 1 << 20 <= A < 1 << 24:
+            continue
+        if np.rint(127.0 * (float(h) * float(w)) / (A * 2.0 ** 24)) != round(Fraction(127 * h * w, A << 24)):
+            found.append((h, w, A))
+    return found
+
+
+@pytest.mark.parametrize("K", [5, 8, 100, 128, 384, 1000, 5119, 12288, 20000, 40000])
+@pytest.mark.parametrize("group", [0, 128])
+def test_borders_that_64_bits_do_not_show(K, group):
+    if K % 128 and group:
+        pytest.skip("a group divides K")
+    print(f"borders K={K} group={group}", flush=True)
+    cases = [(11742707, 12087109, 14819600)] + near_borders(12, 7)
+    for h, w, A in cases:
+        x, ww = torch.zeros((2, K)), torch.full((K,), 1.0)
+        for s in ([0] if not group else range(0, K, 128)):   # every block's
+            x[0, s], ww[s] = A, 2.0 ** 24
+            x[0, s + 3], ww[s + 3] = h, w
+            x[1, s], x[1, s + 3] = -A, -h
+        check(x, ww, group)
 
 
 @pytest.mark.parametrize("K", [4, 17, 128, 512, 1280, 9000, 20000, 40000])
