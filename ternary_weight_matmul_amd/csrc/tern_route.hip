@@ -136,7 +136,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         }
         double w = id >= 0 ? score(mine) : 0.0;
         if (a.renormalize) total = wave_sum(w);
-        w = total == 0.0 ? 0.0 : w / total * (double)a.scale;
+        // none for a place without an expert, whatever the factor and the others' scores are
+        w = total == 0.0 || id < 0 ? 0.0 : w / total * (double)a.scale;
         if (lane < a.top_k) {
             a.ids[t * a.top_k + lane] = id;
             a.weights[t * a.top_k + lane] = (float)w;
