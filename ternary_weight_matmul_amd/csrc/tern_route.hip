@@ -52,7 +52,9 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
             l[i] = e < E ? load_logit(a.logits, a.l_dtype, t * E + e) : ninf;
             most = max(most, order_key(l[i]));
         }
-        const double top = a.sigmoid ? 0.0 : (double)key_value(wave_max(most));
+        // the largest logit; no score of a softmax is a number where that is infinite
+        const float largest = key_value(wave_max(most));
+        const double top = a.sigmoid ? 0.0 : (double)(largest == -ninf ? __builtin_nanf("") : largest);
         // what a logit's score is before the division by `total`
         auto score = [&](float v) __attribute__((always_inline)) {
             return a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : v == ninf ? 0.0 : exp((double)v - top);

@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import q8_util as R  # noqa: E402
-from test_gpu_route import DEV, DT, Layer  # noqa: E402
+from test_gpu_route import DEV, DT, Layer, check  # noqa: E402
 
 tern = pytest.importorskip("ternary_weight_matmul_amd")
 
@@ -18,6 +18,25 @@ INF, NAN = float("inf"), float("nan")
 def _need_gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("groups,keep,best", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_logits_that_are_not_finite(score, biased, groups, keep, best, renorm):
+    """A softmax over +inf or NaN has NaN weights, whichever experts are taken."""
+    E = 32
+    rng = np.random.default_rng(11)
+    lg = torch.from_numpy(rng.standard_normal((6, E))).float()
+    lg[0, 3] = INF
+    lg[1, 29], lg[1, 30] = INF, INF
+    lg[2, 17] = NAN
+    lg[3, 8:] = -INF
+    lg[3, 5] = INF
+    lg[4, :31], lg[4, 31] = -INF, NAN
+    bias = torch.from_numpy(rng.standard_normal(E) * 0.1).float() if biased else None
+    check(lg, 8, score, bias, groups, keep, best, renorm, 2.5)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
