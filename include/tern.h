@@ -73,7 +73,9 @@ typedef enum {
     TERN_PATH_GEMV_FP4 = 4, /* decode kernel with the weights as 4-bit (e2m1 +-2 / 0) matrix-core
                                operands and each bf16 activation split exactly into two e4m3
                                terms with a power-of-two scale per 32 (v_mfma_scale_f32_
-                               16x16x128_f8f6f4); bf16 X only, M <= 4, K <= 32768 */
+                               16x16x128_f8f6f4); bf16 X only, M <= 4, K <= 32768, and no
+                               more weight rows than a launch of fewer than 2^32
+                               threads holds (6 * 10^7 of them are not too many) */
     TERN_PATH_GEMV_B16 = 5  /* decode kernel for batches of up to 16 rows: +-2 / 0 weight
                                operands of v_mfma_f32_16x16x32 against activation fragments
                                held in registers, waves splitting K; M <= 16, K <= 2^20 */

@@ -18,7 +18,8 @@ constexpr int64_t kMaxK = int64_t(1) << 30;
 // of K / 2 bytes).
 constexpr int64_t kMxMaxK = int64_t(1) << 24;
 // Products with 8-bit activations: the same, 128 rows of K bytes; a grid has fewer than 2^32 threads,
-// up to 8 for each row of W with few rows of X, and one for 32 outputs in tiles of 64 x 128.
+// up to 8 for each row of W with few rows of X, and one for 32 outputs in tiles of 64 x 128 (the decode
+// kernel of up to 4 rows has more of them a row, and leaves what is too much for a launch to these).
 constexpr int64_t kQ8MaxK = int64_t(1) << 23, kQ8MaxDim = int64_t(1) << 28, kQ8MaxOut = int64_t(1) << 36;
 constexpr int64_t kMaxProduct = int64_t(1) << 62;
 constexpr size_t kGemvLdsLimit = 152 * 1024;
@@ -229,8 +230,8 @@ bool q8_product_ok(int64_t M, int64_t N, int64_t K) {
 // shortest time by their own estimates.  Measured, in us, few rows / tiles of 64 x 128 / of 128 x 384
 // (estimates in brackets), N x K: 5120 x 5120, 128 rows 15.5 / 27.6 / 62.1 (16 / 28 / 68), 512 rows
 // 51.7 / 39.6 / 65.3 (57 / 41 / 68); 17408 x 5120, 64 rows 36.9 / 28.2 / 66.7 (30 / 28 / 68), 512 rows
-// 182 / 86.9 / 70.7 (223 / 81 / 68); 5120 x 17408, 128 rows 40.9 / 82.1 / 180 (49 / 86 / 188);
-// 1024 x 1024, 1024 rows 7.9 / 9.4 / 25.7 (7 / 8 / 28), 4096 rows 25.6 / 14.3 / 30.5 (21 / 11 / 28).
+// 182 / 86.9 / 70.7 (195 / 81 / 68); 5120 x 17408, 128 rows 40.9 / 82.1 / 180 (49 / 86 / 188);
+// 1024 x 1024, 1024 rows 7.9 / 9.4 / 25.7 (7 / 8 / 28), 4096 rows 25.6 / 14.3 / 30.5 (20 / 11 / 28).
 enum class Q8Kernel { Decode, Rows, Blocks, Tiles };
 Q8Kernel q8_kernel(int64_t M, int64_t N, int64_t K) {
     if (M <= TERN_GEMV_MAX_M && tern::gemv_fp4_fits(M, N, K, 3)) return Q8Kernel::Decode;

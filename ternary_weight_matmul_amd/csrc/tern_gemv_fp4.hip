@@ -458,7 +458,8 @@ hipError_t launch_f4m(const GemmArgs &a, const F4Shape &g) {
 bool gemv_fp4_fits(int64_t M, int64_t N, int64_t K, int x_dtype) {
     if ((x_dtype != 1 && x_dtype != 3) || M < 1 || M > 4 || N < 1 || K < 128) return false;
     const F4Shape g = f4_shape(M, N, K);
-    return g.spw <= F_MAX_SPW && g.q > 0;
+    // a launch has fewer than 2^32 threads: 64 nw for 4 q rows, 32 a row at 5120 x 5120
+    return g.spw <= F_MAX_SPW && g.q > 0 && (int64_t)g.grid * 64 * g.nw < int64_t(1) << 32;
 }
 
 hipError_t launch_gemv_fp4(const GemmArgs &a) {
