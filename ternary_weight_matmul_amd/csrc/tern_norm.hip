@@ -155,10 +155,12 @@ __device__ __forceinline__ uint64_t codes_of(const float (&h)[8], const float (&
 #pragma unroll
             for (int j = 1; j < 8; ++j) hi = i == j ? h[j] : hi, wi = i == j ? w[j] : wi;
             const double p = (double)hi * (double)wi;
-            // an a below the normal range may be a third less than the value that it stands for
-            const int below = (int)fmin(fmax(floor(127.0 * p / (double)a), -128.0), 127.0);
+            // the instruction's estimate is good to 2^-20 at least, and next to an integer either of the codes
+            // beside it will do as `below`
+            const int below = (int)floor(127.0 * p * __builtin_amdgcn_rcp((double)a));
             // (below + 1/2) a is exact, and its difference to 127 p has the right sign
             const double past = __builtin_fma(127.0, p, -((double)below + 0.5) * (double)a);
+            // an a below the normal range may be a third less than the value that it stands for: cut off
             const uint32_t c = (uint32_t)max(min(below + (past > 0.0 || (past == 0.0 && (below & 1))), 127), -127);
 #pragma unroll
             for (int j = 0; j < 8; ++j) n[j] = i == j ? c : n[j];

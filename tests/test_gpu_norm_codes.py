@@ -67,11 +67,8 @@ def near_borders(count, seed):
     return found
 
 
-@pytest.mark.parametrize("K", [5, 8, 100, 128, 384, 1000, 5119, 12288, 20000, 40000])
-@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("K,group", [(K, g) for K in (5, 8, 100, 128, 384, 1000, 5119, 12288, 20000, 40000) for g in (0, 128) if g == 0 or K % g == 0])
 def test_borders_that_64_bits_do_not_show(K, group):
-    if K % 128 and group:
-        pytest.skip("a group divides K")
     print(f"borders K={K} group={group}", flush=True)
     cases = [(11742707, 12087109, 14819600)] + near_borders(12, 7)
     for h, w, A in cases:
@@ -83,12 +80,9 @@ def test_borders_that_64_bits_do_not_show(K, group):
         check(x, ww, group)
 
 
-@pytest.mark.parametrize("K", [4, 17, 128, 512, 1280, 9000, 20000, 40000])
-@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("K,group", [(K, g) for K in (4, 17, 128, 512, 1280, 9000, 20000, 40000) for g in (0, 128) if g == 0 or K % g == 0])
 def test_codes_of_magnitudes_below_the_normal_range(K, group):
     """The largest magnitude as an fp32 is up to a third below the value: its code is 127, not 178."""
-    if K % 128 and group:
-        pytest.skip("a group divides K")
     print(f"small magnitudes K={K} group={group}", flush=True)
     rng = np.random.default_rng(K)
     for top in (1.4, -1.4, 1.49, 2.4, 3.49, -7.4, 12.5, 100.3):
