@@ -318,7 +318,9 @@ tern_status tern_moe(const void *X, tern_dtype x_dtype, const void *logits, tern
  * addition to a residual stream before it:
  *   h = X + residual, rounded to the stream's type and written to residual_out
  *       (without a residual h = X)
- *   Y = h / sqrt(mean of h^2 over the row + eps) * weight, rounded once
+ *   Y = h / sqrt(mean of h^2 over the row + eps) * weight, formed in fp32 (three
+ *       roundings, and what falls below 2^-126 on the way loses bits) and rounded
+ *       to Y's type
  *   codes, scales: the same values as 8-bit activations.  The largest |h weight|
  *       of a row or block is taken as an fp32; beyond that range its scale is NaN.
  *   X, Y of any type; residual and residual_out in X's type or TERN_F32
@@ -337,8 +339,8 @@ tern_status tern_rms_norm(const void *X, tern_dtype x_dtype, const void *residua
 
 /*
  * tern_q8_quantize -- codes and scales of X[M,K] of any type, with q_group 0 for
- * K <= 65536 (TERN_ERR_SHAPE).  tern_q8_dequant -- their values, rounded once to
- * y_dtype.  Element alignment.
+ * K <= 65536 (TERN_ERR_SHAPE).  tern_q8_dequant -- their values, products in fp32,
+ * rounded to y_dtype.  Element alignment.
  */
 tern_status tern_q8_quantize(const void *X, tern_dtype x_dtype, int8_t *codes, float *scales, int32_t q_group,
                              int64_t M, int64_t K, hipStream_t stream);
@@ -368,7 +370,9 @@ tern_status tern_matmul_q8(const int8_t *x_codes, const float *x_scales, int32_t
  *   c = s + bias (fp32 [E]); with bias NULL s, experts in the order of their logits
  *   with groups > 1, groups of E / groups consecutive experts: only the experts of
  *       the keep_groups groups with the largest sums of their group_best (1 or 2)
- *       largest c are open
+ *       largest c are open.  An expert that is never taken does not count, so that
+ *       a group may have a sum of one c; with group_best 1 and bias NULL, groups
+ *       go by their largest logit, with 2 by sums of s
  *   ids [T,top_k] int32: the top_k open experts, largest c first
  *   weights [T,top_k] fp32: their s, divided by the sum of it over the taken ones
  *       if renormalize is not 0 (0 where that sum is 0), times scale

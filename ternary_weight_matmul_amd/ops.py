@@ -396,7 +396,8 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Op
               groups: int = 1, keep_groups: int = 1, group_best: int = 1, renormalize: bool = True, scale: float = 1.0):
     """The experts ids int32 [T,top_k] of every token and their weights fp32 [T,top_k] from logits [T,E]
     (tern_moe_route): softmax or sigmoid scores, chosen by score + bias (fp32 [E]) among the keep_groups of
-    `groups` groups of consecutive experts whose group_best largest add up to the most."""
+    `groups` groups of consecutive experts whose group_best largest add up to the most.  Without a bias
+    experts are chosen by their logits, and so are groups with group_best 1."""
     index = _need_matrix(logits, "logits", _FLOATS)
     T, E = logits.shape
     if score not in _SCORES:
