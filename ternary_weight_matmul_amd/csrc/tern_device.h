@@ -172,4 +172,11 @@ __device__ __forceinline__ float row16_sum(float x) {
     return x;
 }
 
+// The compiler keeps the wave's LDS accesses on their sides.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 }  // namespace tern

@@ -44,7 +44,10 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-template <int WV, int NB, int MB, int ST, bool GX>
+constexpr int WV = 4, NB = 2, MB = 4;   // waves; sixteens of weight rows of a wave, and of rows of X
+constexpr int ST = 3;                   // buffers
+
+template <bool GX>
 struct Shape {
     static constexpr int NT = 64 * WV, BM = 16 * MB, BN = 16 * NB * WV;
     static constexpr int A_LDS = BM * 128, W_LDS = BN * 32;
@@ -55,23 +58,21 @@ struct Shape {
     static constexpr int LOADS = AI + WI;
     static constexpr int SP = (BN + NT - 1) / NT, XP = GX ? (BM + NT - 1) / NT : 0;
     static_assert(A_LDS % (1024 * WV) == 0 && W_LDS % (1024 * WV) == 0, "whole load instructions");
-    static_assert(ST >= 2 && ST <= 4 && ST * BUF <= 160 * 1024, "buffers");
+    static_assert(ST == 3 && ST * BUF <= 160 * 1024, "buffers");
     static_assert((ST - 2) * LOADS < 64, "the wait counter has 6 bits");
 };
 
-template <int WV, int NB, int MB, int ST, bool GX>
+template <bool GX>
 __global__ __launch_bounds__(64 * WV, 2) void q8_blocks_kernel(Q8Args a, int tiles_m, int tiles_n, int vec) {
-    typedef Shape<WV, NB, MB, ST, GX> T;
+    typedef Shape<GX> T;
     // One variable each, so that the compiler sees that an access to one need not wait for the loads
     // into another.
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[T::BUF], buf1[T::BUF];
-    __shared__ __attribute__((aligned(16))) uint8_t buf2[ST > 2 ? T::BUF : 16], buf3[ST > 3 ? T::BUF : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[T::BUF], buf1[T::BUF], buf2[T::BUF];
     auto buf = [&](auto i) TERN_INLINE {
         constexpr int I = decltype(i)::value % ST;
         if constexpr (I == 0) return buf0;
         else if constexpr (I == 1) return buf1;
-        else if constexpr (I == 2) return buf2;
-        else return buf3;
+        else return buf2;
     };
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -195,14 +196,8 @@ __global__ __launch_bounds__(64 * WV, 2) void q8_blocks_kernel(Q8Args a, int til
         wait_and_meet<(ST - 2) * T::LOADS>();   // step s + 1 is there
     };
     auto each = [&](auto f) TERN_INLINE {   // f(0), ..., f(ST - 1) until one returns true
-        typedef std::integral_constant<int, 0> I0;
-        typedef std::integral_constant<int, 1> I1;
-        if (f(I0()) || f(I1())) return true;
-        if constexpr (ST > 2)
-            if (f(std::integral_constant<int, 2>())) return true;
-        if constexpr (ST > 3)
-            if (f(std::integral_constant<int, 3>())) return true;
-        return false;
+        return f(std::integral_constant<int, 0>()) || f(std::integral_constant<int, 1>()) ||
+               f(std::integral_constant<int, 2>());
     };
     load_scales(0);
     each([&](auto i) TERN_INLINE {
@@ -236,13 +231,13 @@ __global__ __launch_bounds__(64 * WV, 2) void q8_blocks_kernel(Q8Args a, int til
     }
 }
 
-template <int WV, int NB, int MB, int ST, bool GX>
+template <bool GX>
 hipError_t launch_t(const Q8Args &a) {
-    typedef Shape<WV, NB, MB, ST, GX> T;
+    typedef Shape<GX> T;
     const int tm = (int)((a.M + T::BM - 1) / T::BM), tn = (int)((a.N + T::BN - 1) / T::BN);
     const size_t unit = a.y_dtype == 2 ? 16 : 8;
     const int vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % unit == 0;
-    hipLaunchKernelGGL((q8_blocks_kernel<WV, NB, MB, ST, GX>), dim3((unsigned)(tm * tn)), dim3(T::NT), 0, a.stream, a, tm, tn,
+    hipLaunchKernelGGL(q8_blocks_kernel<GX>, dim3((unsigned)(tm * tn)), dim3(T::NT), 0, a.stream, a, tm, tn,
                        vec);
     return hipGetLastError();
 }
@@ -255,7 +250,7 @@ double q8_blocks_time(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_q8_blocks(const Q8Args &a) {
-    return a.grouped ? launch_t<4, 2, 4, 3, true>(a) : launch_t<4, 2, 4, 3, false>(a);
+    return a.grouped ? launch_t<true>(a) : launch_t<false>(a);
 }
 
 }  // namespace tern

@@ -55,13 +55,6 @@ typedef float float16v_t __attribute__((ext_vector_type(16)));
 typedef int int8v_t __attribute__((ext_vector_type(8)));
 typedef int int2v_t __attribute__((ext_vector_type(2)));
 
-// The compiler keeps the wave's LDS accesses on their sides.
-__device__ __forceinline__ void wave_order() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 constexpr int T_ROWS = 32;            // rows whose terms lie together
 constexpr int T_BLOCK = 6 * 1024;     // bytes of their terms of one block: [4][lane][16], then [4][lane][8]
 
@@ -94,7 +87,6 @@ __device__ __forceinline__ void pack6(const uint32_t (&c)[8], uint32_t *r) {
     r[5] = (uint32_t)(d[3] >> 16);
 }
 
-// One wave for 32 rows and one block.
 // Terms of 32 rows' block u, by one wave.
 __device__ __forceinline__ void split_terms(const int8_t *Q, char *out, int M, int groups, int64_t u, int lane) {
     const int h = lane >> 5, i = lane & 31;
@@ -183,8 +175,7 @@ struct Shape {
 };
 
 template <int WM, int WN, int MB, int NB, int ST, bool GX>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN > 4 ? 2 : 1) void q8_gemm_kernel(Q8Args a, int tiles_m, int tiles_n,
-                                                                                     int vec) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(Q8Args a, int tiles_m, int tiles_n, int vec) {
     typedef Shape<WM, WN, MB, NB, ST, GX> T;
     // One variable each, so that the compiler sees that an access to one need not wait for the loads
     // into another.

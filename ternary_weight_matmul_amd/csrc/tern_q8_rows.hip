@@ -36,13 +36,6 @@ namespace tern {
 
 namespace {
 
-// The compiler keeps the wave's LDS accesses on their sides.
-__device__ __forceinline__ void wave_order() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 constexpr int min(int a, int b) { return a < b ? a : b; }
 constexpr int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 

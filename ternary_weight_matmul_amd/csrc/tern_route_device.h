@@ -67,11 +67,4 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// The compiler keeps the wave's LDS accesses on their sides.
-__device__ __forceinline__ void wave_order() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 }  // namespace tern

@@ -75,3 +75,23 @@ def test_more_routes_than_experts(T, E, k, xd, yd):
     w = torch.from_numpy(rng.standard_normal((T, k))).float()
     want, bound = L.want(x, ids, w, yd)
     R.assert_close(L.run(x, ids, w, yd), want, bound, "more routes than experts")
+
+
+def test_which_group_comes_first_where_scores_run_out_of_bits():
+    """Sigmoids that are 1 in 64 bits: with one best expert and no bias groups go by logits, with two by scores."""
+    lg = torch.tensor([[45.0, 44.0, 43.0, 42.0, 60.0, 41.0, 42.5, 50.0]]).to(DEV)
+    ids, _ = tern.moe_route(lg, 2, score="sigmoid", groups=2, keep_groups=1, group_best=1)
+    assert ids.tolist() == [[4, 7]]
+    ids, _ = tern.moe_route(lg, 2, score="sigmoid", groups=2, keep_groups=1, group_best=2)
+    assert ids.tolist() == [[0, 1]]
+
+
+def test_a_group_with_one_open_expert_has_that_ones_score():
+    lg = torch.tensor([[-INF, 3.0, -INF, -INF, 0.5, 0.25, 0.0, 0.75], [-INF, -1.0, -INF, -INF, 0.5, 0.25, 0.0, 0.75]]).to(DEV)
+    for bias in (None, torch.zeros(8, device=DEV)):
+        ids, w = tern.moe_route(lg, 3, score="sigmoid", bias=bias, groups=2, keep_groups=1, group_best=2)
+        # 0.95 alone against 0.68 + 0.62, and 0.27 alone
+        assert ids.tolist() == [[7, 4, 5], [7, 4, 5]]
+    lg[0, 4:6], lg[0, 7] = -INF, -INF
+    ids, w = tern.moe_route(lg, 3, score="sigmoid", groups=2, keep_groups=1, group_best=2)
+    assert ids.tolist()[0] == [1, -1, -1] and w[0].tolist()[1:] == [0, 0]   # 0.95 against 0.5
