@@ -87,6 +87,11 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     return v;
 }
 
+// By value: an array, or variables that a lambda refers to, would be indexed in scratch memory.
+__device__ __forceinline__ float pick(int m, float x0, float x1, float x2, float x3) {
+    return m == 0 ? x0 : m == 1 ? x1 : m == 2 ? x2 : x3;
+}
+
 // (steps per wave, quads per workgroup) pairs that are instantiated.
 #define TERN_F4_TABLE(X)                                                                                       \
     X(1, 1) X(1, 2) X(1, 3) X(1, 4) X(1, 5) X(1, 6) X(1, 8) X(1, 9) X(1, 10) X(1, 12) X(1, 17) X(2, 1) X(2, 2) X(2, 3) \
@@ -139,11 +144,9 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
     //         meet zero activations, and their scales are dropped) ----
     uint4 xq[SPW][M];      // 8 bf16, or 8 codes in the first two words
     float xs[SPW][M];      // XQ 2: the blocks' scales
-    float row_scale[M];    // XQ 1
-    if constexpr (XQ == 1) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) row_scale[m] = Rf[m];
-    }
+    // XQ 1: the rows' scales, in scalar registers
+    float x0 = 1.f, x1 = 1.f, x2 = 1.f, x3 = 1.f;
+    if constexpr (XQ == 1) x0 = Rf[0], x1 = Rf[M > 1 ? 1 : 0], x2 = Rf[M > 2 ? 2 : 0], x3 = Rf[M > 3 ? 3 : 0];
 #pragma unroll
     for (int st = 0; st < SPW; ++st) {
         const int k0 = min((wave * SPW + st) * F_STEP + 8 * lane, K - 8);
@@ -321,12 +324,6 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
         const int n = n0 + rr;
         if (n >= N) return;
         if constexpr (XQ == 0) y *= 0.5f;   // the weights were +-2
-        if constexpr (XQ == 1) {
-            float f = row_scale[0];
-#pragma unroll
-            for (int i = 1; i < M; ++i) f = m == i ? row_scale[i] : f;
-            y *= f;
-        }
         if constexpr (S8) y *= Rf[n];
         if (y_dtype == 2) store_out<2>(Y, (int64_t)m * N + n, y);
         else if (y_dtype == 1) store_out<1>(Y, (int64_t)m * N + n, y);
@@ -344,7 +341,7 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
             y = (v[0] + v[1]) + (v[2] + v[3]);
         }
         y = row16_sum(y);
-        if (o < 4 * Q * M && w == 0) finish(m, rr, y);
+        if (o < 4 * Q * M && w == 0) finish(m, rr, XQ == 1 ? y * pick(m, x0, x1, x2, x3) : y);
     } else {
         for (int o = tid; o < 4 * Q * M; o += 64 * nw) {
             const int m = o / (4 * Q);
@@ -355,7 +352,7 @@ __global__ __launch_bounds__(64 * F_MAX_WAVES) void gemv_fp4_kernel(const void *
                 const float4_t v = pp[w * 4 * Q];
                 y += (v[0] + v[1]) + (v[2] + v[3]);
             }
-            finish(m, rr, y);
+            finish(m, rr, XQ == 1 ? y * pick(m, x0, x1, x2, x3) : y);
         }
     }
 }
