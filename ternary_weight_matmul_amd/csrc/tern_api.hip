@@ -269,11 +269,13 @@ tern_status moe(const void *X, tern_dtype x_dtype, const void *logits, tern_dtyp
     if (Y == nullptr) return TERN_ERR_NULL;
     if (!aligned(Y, dtype_size(y_dtype))) return TERN_ERR_ALIGN;
     if (F == 0) return from_hip(tern::launch_fill_zero(Y, T * H * (int64_t)dtype_size(y_dtype), stream));
-    if ((routed ? ids == nullptr || weights == nullptr : logits == nullptr) || X == nullptr || gate_up == nullptr || gate_up_scales == nullptr || down == nullptr ||
-        down_scales == nullptr || workspace == nullptr)
+    if (routed ? ids == nullptr || weights == nullptr : logits == nullptr) return TERN_ERR_NULL;
+    if (X == nullptr || gate_up == nullptr || gate_up_scales == nullptr || down == nullptr || down_scales == nullptr ||
+        workspace == nullptr)
         return TERN_ERR_NULL;
-    if (!aligned(X, 16) || !aligned(logits, dtype_size(l_dtype)) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(gate_up, 16) || !aligned(down, 16) ||
-        !aligned(gate_up_scales, 2) || !aligned(down_scales, 2) || !aligned(workspace, 256))
+    if (!aligned(logits, dtype_size(l_dtype)) || !aligned(ids, 4) || !aligned(weights, 4)) return TERN_ERR_ALIGN;
+    if (!aligned(X, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(gate_up_scales, 2) ||
+        !aligned(down_scales, 2) || !aligned(workspace, 256))
         return TERN_ERR_ALIGN;
     if (workspace_bytes < tern::moe_workspace(T, top_k, H, F)) return TERN_ERR_SHAPE;
     tern::MoeArgs a;

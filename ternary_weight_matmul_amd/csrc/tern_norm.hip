@@ -26,9 +26,14 @@
 // longer ones one each.
 //
 // Bound: HBM where there are thousands of rows (2048 x 5120 with a residual stream
-// 18.3 us, 4.6 TB/s, a copy of as much 19.1), else the way of the first row's lines
-// from memory, and with 8-bit outputs the vector instructions, 15 a value
-// (333 x 17408 20.8 us, 3.1 TB/s).
+// 20.9 us, 4.0 TB/s, inputs and outputs over more than the last-level cache), else
+// the way of the first row's lines from memory.  With 8-bit outputs it is the vector
+// instructions and what they wait for, one after the other: 2048 x 5120 takes 24.5
+// us, of which 31 instructions a value (squares in 64 bits, codes) keep a SIMD busy
+// for 8, and the 10 waves of a CU wait for memory or for each other for 53% of their
+// time.  Above 12288 values there is one workgroup a CU, and nothing of its next row
+// on the way: 333 x 17408 22.9 us (the copy's rate gives 11.9), two rows one after
+// the other on 77 of the CUs; 2048 x 17408 without a norm 67 (20.0).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -339,9 +344,9 @@ __global__ __launch_bounds__(MOST) void norm_kernel(NormArgs a) {
 }
 
 // Rows too long for registers: a workgroup of 1024 reads one twice, the second time from the L2 (64 rows of
-// 65536 to 8 bits 46 us; with what did not fit in registers in scratch memory 72).  8 values
-// a thread in turn, 4 turns' asked for at once; the last ones one by one, as the stream may be written in
-// place and no value may be read after that as if it were x or r.
+// 65536 to 8 bits 37 us; read once, with 94 to 160 registers in scratch memory, 1.6 times as long.  Two
+// registers still are there).  8 values a thread in turn, 4 turns' asked for at once; the last ones one by
+// one, as the stream may be written in place and no value may be read after that as if it were x or r.
 template <int XT, int RT>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     constexpr int NT = 1024, TOGETHER = 4;
@@ -501,8 +506,8 @@ hipError_t launch_t(const NormArgs &a) {
     const int threads = TPR > 0 ? MOST : (int)((a.K + 512 * NV - 1) / (512 * NV)) * 64;
     constexpr int ROWS = TPR > 0 ? MOST / TPR : 1;
     // Up to 16 waves a CU, in as many workgroups as give the busiest CU the fewest rows: 2048 x 5120 with
-    // a residual took 18.3 us, against 22.3 with up to 20 waves, and 20.9 with the most workgroups of 16
-    // waves that there is room for.
+    // a residual took 18.3 us (outputs in the cache), against 22.3 with up to 20 waves, and 20.9 with the
+    // most workgroups of 16 waves that there is room for.
     const int64_t need = (a.M + ROWS - 1) / ROWS;
     int64_t grid = 0, least = 0;
     for (int64_t c = std::max(16 * 64 / threads, 1); c >= 1; --c) {
@@ -515,8 +520,8 @@ hipError_t launch_t(const NormArgs &a) {
 }
 
 // Two eights a thread up to 8192, which leaves room for many waves (three: 2048 x 8192 29.7 us against
-// 25.4, 2048 x 5119 24.5 against 21.8, 4096 x 6144 without a residual 19.9 against 22.6), then as few as
-// the workgroup's threads allow.
+// 25.4, 2048 x 5119 24.5 against 21.8), then as few as the workgroup's threads allow.  Without a residual
+// three would gain at some sizes (4096 x 6144 19.9 against 22.6); they follow the same rule.
 template <int XT, int RT>
 hipError_t launch_row(const NormArgs &a) {
     if (a.K <= 128) return launch_t<XT, RT, 16, 1, 256>(a);

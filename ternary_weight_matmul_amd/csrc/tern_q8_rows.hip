@@ -22,7 +22,7 @@
 //
 // Bound: the lines' way from HBM and the decoding of the codes, some 200 vector
 // instructions a wave and step, which overlap only in part.  16 rows, 5120 -> 5120,
-// 5120 -> 17408 and 17408 -> 5120: 7.9, 13.2 and 16.6 us; the loads alone 6.5, 9.9 and
+// 5120 -> 17408 and 17408 -> 5120: 8.1, 13.2 and 17.0 us; the loads alone 6.5, 9.9 and
 // 12.9, the codes' alone 5.4, 8.8 and 9.7, of which 2 are the launch.
 #include <hip/hip_runtime.h>
 

@@ -69,3 +69,11 @@ def test_up_to_four_rows(M, N, group):
 def test_tiles_in_runs(M, N, K, group):
     assert (tern.lib.tern_matmul_q8_workspace(M, N, K) > 0) == (K == 2816)
     check(M, N, K, group, "bf16")
+
+
+# large tiles with fewer blocks of K than they have buffers: one, two, three
+@pytest.mark.parametrize("M,N,K", [(30700, 26877, 128), (20000, 26877, 256), (16300, 19197, 384)])
+@pytest.mark.parametrize("group", [0, 128])
+def test_large_tiles_of_few_blocks(M, N, K, group):
+    assert tern.lib.tern_matmul_q8_workspace(M, N, K) > 0
+    check(M, N, K, group, "bf16")
